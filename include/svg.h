@@ -51,7 +51,7 @@ typedef enum svg_status {
   SVG_ERR_INVALID_ARG = 1,   /* null pointer, bad size, misaligned tensor, bad kind */
   SVG_ERR_UNSUPPORTED = 2,   /* head_dim not in {64,128}, block size not in {64,128},
                                 not an sm_100 device */
-  SVG_ERR_CAPACITY = 3,      /* caller buffer too small (col_capacity, workspace) */
+  SVG_ERR_CAPACITY = 3,      /* caller buffer too small (col_capacity, workspace, cache pages) */
   SVG_ERR_CUDA = 4,          /* a CUDA runtime/driver call failed */
   SVG_ERR_DEVICE_TIMEOUT = 5 /* a device-side bounded wait ran out (see svg_get_device_status) */
 } svg_status;
@@ -475,12 +475,160 @@ svg_status svg2_sparse_attention(int32_t BH, int32_t N, int32_t d, int32_t block
                                  const int32_t* row_ptr, const int32_t* col_idx, svg_bf16* os,
                                  float* lse, svg_stream_t stream);
 
+/* ===========================================================================
+ * History cache: keys and values of rows made earlier, in pages
+ * A generator that makes a video chunk by chunk attends from each new chunk to
+ * the frames made before, whose keys and values it keeps; several
+ * continuations of one history share them. No counterpart on the pages: the
+ * dense mask of svg_sparse_attention takes every sample's own K and V in full.
+ *
+ * Pool      k_pages, v_pages: bf16 [n_pages, H_kv, page_size, d], 16-byte
+ *           aligned, one pair per layer.
+ * State     one set for all layers, device int32, 16-byte aligned:
+ *             table [max_seqs, max_pages]  page of each run of page_size rows
+ *                                          of a sequence; -1: none
+ *             lens  [max_seqs]             rows of each sequence
+ *             refs  [n_pages]              sequences that hold each page; a
+ *                                          page with 0 is free
+ *           Written by svg_cache_reset first, then by these calls alone.
+ *           Free pages are handed out lowest number first, so the state after
+ *           a call depends on the state before it and its arguments alone.
+ * Lists     seqs, src, dst: device int32 [n], 1 <= n <= 1024, sequence numbers in
+ *           [0, max_seqs). A negative number is an idle entry (a padded
+ *           batch) and does nothing. An entry refused on the device sets the
+ *           bounds bit and changes nothing: a number past the end, a sequence
+ *           named twice (the first one counts), a length or page in the state
+ *           that cannot be.
+ * Order     calls on one state and the layers' pools are ordered by their
+ *           stream; two streams need the caller's own ordering.
+ * Errors    INVALID_ARG (null, misaligned, sizes < 1, n > 1024, n_pages > 2^24,
+ *           max_pages * page_size > 2^30, max_seqs * max_pages or
+ *           n_pages * H_kv * page_size > 2^31 - 1), UNSUPPORTED (head_dim not 64 or
+ *           128, page_size not 16, 32, 64, 128 or 256), CUDA.
+ * ------------------------------------------------------------------------ */
+typedef struct svg_cache_geom {
+  int32_t n_pages, page_size; /* pages of the pool, rows of a page */
+  int32_t H_kv, head_dim;     /* heads of keys and values (<= 65535), 64 or 128 */
+  int32_t max_seqs, max_pages; /* rows and columns of the page table */
+} svg_cache_geom;
+
+/* svg_cache_reset -- every page free, every sequence empty. */
+svg_status svg_cache_reset(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
+                           int32_t* refs, svg_stream_t stream);
+
+/* svg_cache_fork -- sequence dst[i] becomes a copy of src[i] that shares all its
+ * pages (no row is copied; svg_cache_reserve gives a sequence its own copy of
+ * a shared, partly filled last page before it grows). One source may have many
+ * targets. dst[i] must be empty and must not be a source of the same call:
+ * refused otherwise. */
+svg_status svg_cache_fork(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
+                          int32_t* refs, const int32_t* src, const int32_t* dst, int32_t n,
+                          svg_stream_t stream);
+
+/* svg_cache_free -- sequence seqs[i] keeps its first keep[i] rows (device int32
+ * [n]; NULL: none); the pages past them are given up and are free once no
+ * sequence holds them. keep[i] at or above the length changes nothing, a negative one is
+ * refused. */
+svg_status svg_cache_free(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
+                          int32_t* refs, const int32_t* seqs, const int32_t* keep, int32_t n,
+                          svg_stream_t stream);
+
+/* svg_cache_reserve -- room for counts[i] more rows of sequence seqs[i]: pages
+ * are added to its table row and its length grows. A partly filled last page
+ * that another sequence held too when the call began is replaced by a new one
+ * (whose rows svg_cache_write copies). All or nothing: when the pool has too few free
+ * pages for the whole call, nothing is reserved and the capacity bit is set
+ * (svg_get_device_status). An entry that would outgrow max_pages * page_size
+ * is left out, with the capacity bit, and the others are served.
+ *   counts   device int32 [n], >= 0.
+ *   plan     device int32 [n, 4] out, for svg_cache_write: the first new row,
+ *            the number of new rows (0 where nothing was reserved), the
+ *            replaced page and its replacement (-1, -1: none). */
+svg_status svg_cache_reserve(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
+                             int32_t* refs, const int32_t* seqs, const int32_t* counts,
+                             int32_t n, int32_t* plan, svg_stream_t stream);
+
+/* svg_cache_write -- one layer's rows into the reserved places: the first plan[i].count
+ * rows of k_new[i], v_new[i], and the rows of a replaced page that the
+ * sequence keeps. May be called again with other rows while the plan and the table stand
+ * (each denoising step of a chunk rewrites the chunk's rows).
+ *   seqs, plan   as given to and written by svg_cache_reserve.
+ *   k_new, v_new device bf16 [n, H_kv, L, d], 16-byte aligned, not in the pool;
+ *                L >= 1 rows an entry, counts above L are refused. */
+svg_status svg_cache_write(const svg_cache_geom* geom, const int32_t* table, const int32_t* seqs,
+                           const int32_t* plan, int32_t n, int32_t L, const svg_bf16* k_new,
+                           const svg_bf16* v_new, svg_bf16* k_pages, svg_bf16* v_pages,
+                           svg_stream_t stream);
+
+/* svg_cache_compact -- renumbers the pages so that those in use are the lowest:
+ * of the M pages in use, the i-th numbered M or above takes the number of the
+ * i-th free one below M. Writes the table and the counts after the change and
+ * the list of moves; svg_cache_copy_pages then moves each layer's pages.
+ *   table_out, refs_out  out; may be table and refs themselves.
+ *   moves    device int32 [2 + 2 * n_pages] out: the number m of moves
+ *            (<= n_pages / 2), M, then m pairs (from, to); the rest is scratch.
+ * A table entry that names a page not in use becomes -1 and sets the bounds bit. */
+svg_status svg_cache_compact(const svg_cache_geom* geom, const int32_t* table,
+                             const int32_t* refs, int32_t* table_out, int32_t* refs_out,
+                             int32_t* moves, svg_stream_t stream);
+
+/* svg_cache_copy_pages -- copies whole pages of one layer: page moves[2 + 2i] of
+ * k_src and v_src to page moves[3 + 2i] of k_dst and v_dst, i < moves[0]
+ * (a list laid out as svg_cache_compact's; moves[1] is not read). The
+ * destination pool may be the source pool if no page is both a source and a
+ * target; a page named twice as a target ends with the rows of either source.
+ *   max_moves  1 <= max_moves <= n_pages: pairs the list has room for; moves[0] above it
+ *              sets the bounds bit and only that many are copied. */
+svg_status svg_cache_copy_pages(const svg_cache_geom* geom, const int32_t* moves,
+                                int32_t max_moves, const svg_bf16* k_src, const svg_bf16* v_src,
+                                svg_bf16* k_dst, svg_bf16* v_dst, svg_stream_t stream);
+
+/* svg_prefix_attention_workspace_bytes -- host only: device workspace
+ * svg_prefix_attention needs for B entries of Lq query rows and H heads. */
+svg_status svg_prefix_attention_workspace_bytes(const svg_cache_geom* geom, int32_t B, int32_t H,
+                                                int32_t Lq, size_t* bytes);
+
+/* svg_prefix_attention -- attention of B sequences over the history they share
+ * and each one's own rows after it. For entry b with sequence s = seqs[b], query
+ * row i and head h (key head h / (H / H_kv)), the keys are rows
+ * [0, prefix_len) of sequence prefix_seq and rows [prefix_len, lens[s]) of
+ * sequence s:
+ *   O[b,h,i] = sum_j softmax_j(scale * q[b,h,i] . k_j) v_j,
+ * accumulated in fp32, rounded to bf16. Where the entries have few query rows,
+ * the rows of all of them are gathered into tiles and the shared keys and
+ * values are read once for all; a fork of one history gives such sequences.
+ * The prefix need not end with a page. Rows past a sequence's
+ * end are never used, whatever they hold (NaN included).
+ *   prefix_seq   sequence whose first prefix_len rows are shared; may be one of
+ *                the batch. Not read when prefix_len is 0.
+ *   q, o         device bf16 [B, H, Lq, d], 16-byte aligned, not overlapping.
+ *   lse          device float [B, H, Lq] out (natural log) or NULL.
+ *   seqs         device int32 [B]; the same sequence may be named more than
+ *                once; the rows of o and lse of an entry with a negative number are
+ *                left as they are. A row without keys gets O = 0, lse = -inf.
+ *   workspace    device, 256-byte aligned; in use until the call's work ends.
+ * A number past the end of the table, a length that cannot be, or a
+ * prefix_seq shorter than prefix_len sets the bounds bit; the entry's rows are
+ * left as they are (with a bad prefix, every row is). A page number past the
+ * pool sets it too, and its rows count as zeros.
+ * Same results on every call: no atomics in the arithmetic.
+ * Errors: as above, and INVALID_ARG (B < 1 or > 2048, Lq < 1, H not a multiple
+ * of H_kv, B * H * Lq > 2^31 - 1, prefix_len not in [0, max_pages * page_size],
+ * prefix_seq not in [0, max_seqs), scale), CAPACITY (workspace). */
+svg_status svg_prefix_attention(const svg_cache_geom* geom, int32_t B, int32_t H, int32_t Lq,
+                                int32_t prefix_seq, int32_t prefix_len, float scale,
+                                const svg_bf16* q, const svg_bf16* k_pages,
+                                const svg_bf16* v_pages, const int32_t* table,
+                                const int32_t* lens, const int32_t* seqs, svg_bf16* o, float* lse,
+                                void* workspace, size_t workspace_bytes, svg_stream_t stream);
+
 /* ---------------------------------------------------------------------------
  * svg_get_device_status -- synchronises `stream`, then reads and clears the
  * device status bits of the current device (1 = a bounded wait ran out,
- * 2 = an out-of-range index from caller memory was skipped) into *bits
- * (may be NULL). Returns SVG_ERR_DEVICE_TIMEOUT if bit 1 was set,
- * SVG_ERR_INVALID_ARG if only bit 2 was set, SVG_ERR_CUDA on a CUDA error
+ * 2 = an out-of-range index from caller memory was skipped, 4 = a history
+ * cache had no room for the rows asked for) into *bits (may be NULL). Returns
+ * SVG_ERR_DEVICE_TIMEOUT if bit 1 was set, else SVG_ERR_INVALID_ARG if bit 2
+ * was, else SVG_ERR_CAPACITY if bit 4 was, SVG_ERR_CUDA on a CUDA error
  * (including errors of earlier asynchronous launches), SVG_OK otherwise.
  */
 svg_status svg_get_device_status(svg_stream_t stream, int32_t* bits);

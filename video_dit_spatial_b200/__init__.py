@@ -40,6 +40,9 @@ EXPORTED = [
     "svg2_kmeans_workspace_bytes", "svg2_kmeans", "svg2_kmeans_step", "svg2_select_clusters",
     "svg2_build_tile_csr", "svg2_gather_rows", "svg2_scatter_rows", "svg2_sparse_attention",
     "svg2_cluster_value_stats", "svg2_ear_workspace_bytes", "svg2_ear_compensate",
+    "svg_cache_reset", "svg_cache_fork", "svg_cache_free", "svg_cache_reserve", "svg_cache_write",
+    "svg_cache_compact", "svg_cache_copy_pages", "svg_prefix_attention_workspace_bytes",
+    "svg_prefix_attention",
     "svg_status_string", "svg_version",
 ]
 
@@ -77,9 +80,18 @@ class Geom(ctypes.Structure):
                    wl.spatial_band, wl.temporal_width, wl.scale)
 
 
+class CacheGeom(ctypes.Structure):
+    """svg_cache_geom: sizes of a history cache."""
+
+    _fields_ = [("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("H_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("max_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _c_geom_p = ctypes.POINTER(Geom)
+_c_cache_p = ctypes.POINTER(CacheGeom)
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
@@ -121,6 +133,17 @@ def load() -> ctypes.CDLL:
         "svg2_gather_rows": [_i32, _i32, _i32, _vp, _vp, _vp, _vp],
         "svg2_scatter_rows": [_i32, _i32, _i32, _vp, _vp, _vp, _vp],
         "svg2_sparse_attention": [_i32, _i32, _i32, _i32, ctypes.c_float] + [_vp] * 8,
+        "svg_cache_reset": [_c_cache_p] + [_vp] * 4,
+        "svg_cache_fork": [_c_cache_p] + [_vp] * 5 + [_i32, _vp],
+        "svg_cache_free": [_c_cache_p] + [_vp] * 5 + [_i32, _vp],
+        "svg_cache_reserve": [_c_cache_p] + [_vp] * 5 + [_i32, _vp, _vp],
+        "svg_cache_write": [_c_cache_p] + [_vp] * 3 + [_i32, _i32] + [_vp] * 5,
+        "svg_cache_compact": [_c_cache_p] + [_vp] * 6,
+        "svg_cache_copy_pages": [_c_cache_p, _vp, _i32] + [_vp] * 5,
+        "svg_prefix_attention_workspace_bytes": [_c_cache_p, _i32, _i32, _i32,
+                                                 ctypes.POINTER(_sz)],
+        "svg_prefix_attention": [_c_cache_p] + [_i32] * 5 + [ctypes.c_float] + [_vp] * 9 +
+                                [_sz, _vp],
         "svg_status_string": [_i32],
         "svg_version": [],
     }
@@ -349,3 +372,114 @@ def svg2_sparse_attention(BH, N, d, block_k, scale, qs, ks, vs, row_ptr, col_idx
     _check("svg2_sparse_attention", load().svg2_sparse_attention(
         BH, N, d, block_k, scale, _ptr(qs), _ptr(ks), _ptr(vs), _ptr(row_ptr), _ptr(col_idx),
         _ptr(os), _ptr(lse), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# history cache and the attention that reads it
+# ---------------------------------------------------------------------------
+def _buf(name: str, x, dtype: str, numel: int) -> Optional[int]:
+    """Device address of a buffer of the history cache: as _ptr, and a tensor
+    must be on the current device, of the given type and large enough (the
+    kernels take sizes from the geometry, not from the tensor)."""
+    ptr = _ptr(x)
+    if x is None or isinstance(x, int):
+        return ptr
+    import torch
+    if x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {x.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if x.dtype != getattr(torch, dtype):
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.numel() < numel:
+        raise ValueError(f"{name} needs {numel} values, got {x.numel()}")
+    return ptr
+
+
+def _state(geom: CacheGeom, table, lens, refs):
+    return (_buf("table", table, "int32", geom.max_seqs * geom.max_pages),
+            _buf("lens", lens, "int32", geom.max_seqs),
+            _buf("refs", refs, "int32", geom.n_pages))
+
+
+def _pool(geom: CacheGeom, **pages):
+    n = geom.n_pages * geom.H_kv * geom.page_size * geom.head_dim
+    return [_buf(name, x, "bfloat16", n) for name, x in pages.items()]
+
+
+def svg_cache_reset(geom: CacheGeom, table, lens, refs, stream=None) -> None:
+    _check("svg_cache_reset", load().svg_cache_reset(
+        ctypes.byref(geom), *_state(geom, table, lens, refs), _stream(stream)))
+
+
+def svg_cache_fork(geom: CacheGeom, table, lens, refs, src, dst, n=None, stream=None) -> None:
+    n = src.numel() if n is None else n
+    _check("svg_cache_fork", load().svg_cache_fork(
+        ctypes.byref(geom), *_state(geom, table, lens, refs), _buf("src", src, "int32", n),
+        _buf("dst", dst, "int32", n), n, _stream(stream)))
+
+
+def svg_cache_free(geom: CacheGeom, table, lens, refs, seqs, keep=None, n=None,
+                   stream=None) -> None:
+    n = seqs.numel() if n is None else n
+    _check("svg_cache_free", load().svg_cache_free(
+        ctypes.byref(geom), *_state(geom, table, lens, refs), _buf("seqs", seqs, "int32", n),
+        _buf("keep", keep, "int32", n), n, _stream(stream)))
+
+
+def svg_cache_reserve(geom: CacheGeom, table, lens, refs, seqs, counts, plan, n=None,
+                      stream=None) -> None:
+    n = seqs.numel() if n is None else n
+    _check("svg_cache_reserve", load().svg_cache_reserve(
+        ctypes.byref(geom), *_state(geom, table, lens, refs), _buf("seqs", seqs, "int32", n),
+        _buf("counts", counts, "int32", n), n, _buf("plan", plan, "int32", 4 * n),
+        _stream(stream)))
+
+
+def svg_cache_write(geom: CacheGeom, table, seqs, plan, L, k_new, v_new, k_pages, v_pages,
+                    n=None, stream=None) -> None:
+    n = seqs.numel() if n is None else n
+    rows = n * geom.H_kv * L * geom.head_dim
+    _check("svg_cache_write", load().svg_cache_write(
+        ctypes.byref(geom), _buf("table", table, "int32", geom.max_seqs * geom.max_pages),
+        _buf("seqs", seqs, "int32", n), _buf("plan", plan, "int32", 4 * n), n, L,
+        _buf("k_new", k_new, "bfloat16", rows), _buf("v_new", v_new, "bfloat16", rows),
+        *_pool(geom, k_pages=k_pages, v_pages=v_pages), _stream(stream)))
+
+
+def svg_cache_compact(geom: CacheGeom, table, refs, table_out, refs_out, moves,
+                      stream=None) -> None:
+    entries = geom.max_seqs * geom.max_pages
+    _check("svg_cache_compact", load().svg_cache_compact(
+        ctypes.byref(geom), _buf("table", table, "int32", entries),
+        _buf("refs", refs, "int32", geom.n_pages), _buf("table_out", table_out, "int32", entries),
+        _buf("refs_out", refs_out, "int32", geom.n_pages),
+        _buf("moves", moves, "int32", 2 + 2 * geom.n_pages), _stream(stream)))
+
+
+def svg_cache_copy_pages(geom: CacheGeom, moves, max_moves, k_src, v_src, k_dst, v_dst,
+                         stream=None) -> None:
+    _check("svg_cache_copy_pages", load().svg_cache_copy_pages(
+        ctypes.byref(geom), _buf("moves", moves, "int32", 2 + 2 * max_moves), max_moves,
+        *_pool(geom, k_src=k_src, v_src=v_src, k_dst=k_dst, v_dst=v_dst), _stream(stream)))
+
+
+def svg_prefix_attention_workspace_bytes(geom: CacheGeom, B: int, H: int, Lq: int) -> int:
+    out = _sz(0)
+    _check("svg_prefix_attention_workspace_bytes", load().svg_prefix_attention_workspace_bytes(
+        ctypes.byref(geom), B, H, Lq, ctypes.byref(out)))
+    return out.value
+
+
+def svg_prefix_attention(geom: CacheGeom, B, H, Lq, prefix_seq, prefix_len, scale, q, k_pages,
+                         v_pages, table, lens, seqs, o, lse, workspace, workspace_bytes=None,
+                         stream=None) -> None:
+    rows = B * H * Lq
+    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    _check("svg_prefix_attention", load().svg_prefix_attention(
+        ctypes.byref(geom), B, H, Lq, prefix_seq, prefix_len, scale,
+        _buf("q", q, "bfloat16", rows * geom.head_dim),
+        *_pool(geom, k_pages=k_pages, v_pages=v_pages),
+        _buf("table", table, "int32", geom.max_seqs * geom.max_pages),
+        _buf("lens", lens, "int32", geom.max_seqs), _buf("seqs", seqs, "int32", B),
+        _buf("o", o, "bfloat16", rows * geom.head_dim), _buf("lse", lse, "float32", rows),
+        _ptr(workspace), wb, _stream(stream)))

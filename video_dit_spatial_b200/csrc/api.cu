@@ -726,6 +726,201 @@ svg_status svg2_sparse_attention(int32_t BH, int32_t N, int32_t d, int32_t block
   return err == cudaSuccess ? SVG_OK : SVG_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------------------
+// history cache
+// ---------------------------------------------------------------------------
+static svg_status check_cache(const svg_cache_geom* g, svg::CacheDims* c) {
+  if (g == nullptr) return SVG_ERR_INVALID_ARG;
+  if (g->n_pages < 1 || g->page_size < 1 || g->H_kv < 1 || g->head_dim < 1 || g->max_seqs < 1 ||
+      g->max_pages < 1)
+    return SVG_ERR_INVALID_ARG;
+  if (g->head_dim != 64 && g->head_dim != 128) return SVG_ERR_UNSUPPORTED;
+  if (g->page_size != 16 && g->page_size != 32 && g->page_size != 64 && g->page_size != 128 &&
+      g->page_size != 256)
+    return SVG_ERR_UNSUPPORTED;
+  if (g->n_pages > (1 << 24) || g->H_kv > 65535) return SVG_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(g->max_pages) * g->page_size > (1 << 30) ||
+      static_cast<int64_t>(g->max_seqs) * g->max_pages > 0x7fffffffLL ||
+      static_cast<int64_t>(g->n_pages) * g->page_size > 0x7fffffffLL / g->H_kv)
+    return SVG_ERR_INVALID_ARG;
+  *c = svg::CacheDims{g->n_pages, g->page_size, g->H_kv, g->head_dim, g->max_seqs, g->max_pages};
+  return SVG_OK;
+}
+
+// Geometry, state pointers and list length of a bookkeeping call, then the device.
+static svg_status cache_common(const svg_cache_geom* geom, svg::CacheDims* c, int32_t n,
+                               const void* const* state, int n_state, const void* const* lists,
+                               int n_lists, int** status) {
+  for (int i = 0; i < n_state; ++i)
+    if (state[i] == nullptr || !svg::aligned16(state[i])) return SVG_ERR_INVALID_ARG;
+  for (int i = 0; i < n_lists; ++i)
+    if (lists[i] == nullptr || (reinterpret_cast<uintptr_t>(lists[i]) & 3u) != 0)
+      return SVG_ERR_INVALID_ARG;
+  if (n < 1 || n > 1024) return SVG_ERR_INVALID_ARG;
+  svg_status st = check_cache(geom, c);
+  if (st != SVG_OK) return st;
+  if ((st = svg::check_device()) != SVG_OK) return st;
+  cudaError_t err;
+  *status = svg::device_status_word(&err);
+  return *status == nullptr ? SVG_ERR_CUDA : SVG_OK;
+}
+
+svg_status svg_cache_reset(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
+                           int32_t* refs, svg_stream_t stream) {
+  const void* state[3] = {table, lens, refs};
+  svg::CacheDims c;
+  int* status = nullptr;
+  const svg_status st = cache_common(geom, &c, 1, state, 3, nullptr, 0, &status);
+  if (st != SVG_OK) return st;
+  return svg::launch_cache_reset(c, table, lens, refs, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? SVG_OK
+             : SVG_ERR_CUDA;
+}
+
+svg_status svg_cache_fork(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
+                          int32_t* refs, const int32_t* src, const int32_t* dst, int32_t n,
+                          svg_stream_t stream) {
+  const void* state[3] = {table, lens, refs};
+  const void* lists[2] = {src, dst};
+  svg::CacheDims c;
+  int* status = nullptr;
+  const svg_status st = cache_common(geom, &c, n, state, 3, lists, 2, &status);
+  if (st != SVG_OK) return st;
+  return svg::launch_cache_fork(c, table, lens, refs, src, dst, n, status,
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SVG_OK
+             : SVG_ERR_CUDA;
+}
+
+svg_status svg_cache_free(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
+                          int32_t* refs, const int32_t* seqs, const int32_t* keep, int32_t n,
+                          svg_stream_t stream) {
+  const void* state[3] = {table, lens, refs};
+  const void* lists[2] = {seqs, keep};
+  svg::CacheDims c;
+  int* status = nullptr;
+  const svg_status st =
+      cache_common(geom, &c, n, state, 3, lists, keep != nullptr ? 2 : 1, &status);
+  if (st != SVG_OK) return st;
+  return svg::launch_cache_free(c, table, lens, refs, seqs, keep, n, status,
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SVG_OK
+             : SVG_ERR_CUDA;
+}
+
+svg_status svg_cache_reserve(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
+                             int32_t* refs, const int32_t* seqs, const int32_t* counts,
+                             int32_t n, int32_t* plan, svg_stream_t stream) {
+  const void* state[3] = {table, lens, refs};
+  const void* lists[3] = {seqs, counts, plan};
+  svg::CacheDims c;
+  int* status = nullptr;
+  const svg_status st = cache_common(geom, &c, n, state, 3, lists, 3, &status);
+  if (st != SVG_OK) return st;
+  return svg::launch_cache_reserve(c, table, lens, refs, seqs, counts, n, plan, status,
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SVG_OK
+             : SVG_ERR_CUDA;
+}
+
+svg_status svg_cache_write(const svg_cache_geom* geom, const int32_t* table, const int32_t* seqs,
+                           const int32_t* plan, int32_t n, int32_t L, const svg_bf16* k_new,
+                           const svg_bf16* v_new, svg_bf16* k_pages, svg_bf16* v_pages,
+                           svg_stream_t stream) {
+  const void* state[5] = {table, k_new, v_new, k_pages, v_pages};
+  const void* lists[2] = {seqs, plan};
+  if (L < 1 || L > (1 << 30)) return SVG_ERR_INVALID_ARG;
+  svg::CacheDims c;
+  int* status = nullptr;
+  const svg_status st = cache_common(geom, &c, n, state, 5, lists, 2, &status);
+  if (st != SVG_OK) return st;
+  return svg::launch_cache_write(c, table, seqs, plan, n, L, k_new, v_new, k_pages, v_pages,
+                                 status, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SVG_OK
+             : SVG_ERR_CUDA;
+}
+
+svg_status svg_cache_compact(const svg_cache_geom* geom, const int32_t* table,
+                             const int32_t* refs, int32_t* table_out, int32_t* refs_out,
+                             int32_t* moves, svg_stream_t stream) {
+  const void* state[4] = {table, refs, table_out, refs_out};
+  const void* lists[1] = {moves};
+  svg::CacheDims c;
+  int* status = nullptr;
+  const svg_status st = cache_common(geom, &c, 1, state, 4, lists, 1, &status);
+  if (st != SVG_OK) return st;
+  return svg::launch_cache_compact(c, table, refs, table_out, refs_out, moves, status,
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SVG_OK
+             : SVG_ERR_CUDA;
+}
+
+svg_status svg_cache_copy_pages(const svg_cache_geom* geom, const int32_t* moves,
+                                int32_t max_moves, const svg_bf16* k_src, const svg_bf16* v_src,
+                                svg_bf16* k_dst, svg_bf16* v_dst, svg_stream_t stream) {
+  const void* state[4] = {k_src, v_src, k_dst, v_dst};
+  const void* lists[1] = {moves};
+  if (geom == nullptr || max_moves < 1 || max_moves > geom->n_pages) return SVG_ERR_INVALID_ARG;
+  svg::CacheDims c;
+  int* status = nullptr;
+  const svg_status st = cache_common(geom, &c, 1, state, 4, lists, 1, &status);
+  if (st != SVG_OK) return st;
+  return svg::launch_cache_copy(c, moves, max_moves, k_src, v_src, k_dst, v_dst, status,
+                                static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SVG_OK
+             : SVG_ERR_CUDA;
+}
+
+static svg_status check_prefix_shape(const svg_cache_geom* geom, svg::CacheDims* c, int32_t B,
+                                     int32_t H, int32_t Lq) {
+  const svg_status st = check_cache(geom, c);
+  if (st != SVG_OK) return st;
+  if (B < 1 || B > 2048 || H < 1 || Lq < 1 || H % c->H_kv != 0) return SVG_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(B) * H > 0x7fffffffLL / Lq) return SVG_ERR_INVALID_ARG;
+  return SVG_OK;
+}
+
+svg_status svg_prefix_attention_workspace_bytes(const svg_cache_geom* geom, int32_t B, int32_t H,
+                                                int32_t Lq, size_t* bytes) {
+  if (bytes == nullptr) return SVG_ERR_INVALID_ARG;
+  svg::CacheDims c;
+  const svg_status st = check_prefix_shape(geom, &c, B, H, Lq);
+  if (st != SVG_OK) return st;
+  *bytes = svg::prefix_workspace_bytes(c, B, H, Lq);
+  return SVG_OK;
+}
+
+svg_status svg_prefix_attention(const svg_cache_geom* geom, int32_t B, int32_t H, int32_t Lq,
+                                int32_t prefix_seq, int32_t prefix_len, float scale,
+                                const svg_bf16* q, const svg_bf16* k_pages,
+                                const svg_bf16* v_pages, const int32_t* table,
+                                const int32_t* lens, const int32_t* seqs, svg_bf16* o, float* lse,
+                                void* workspace, size_t workspace_bytes, svg_stream_t stream) {
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0)
+    return SVG_ERR_INVALID_ARG;
+  svg::CacheDims c;
+  svg_status st = check_prefix_shape(geom, &c, B, H, Lq);
+  if (st != SVG_OK) return st;
+  if (prefix_seq < 0 || prefix_seq >= c.max_seqs || prefix_len < 0 || prefix_len > c.max_rows())
+    return SVG_ERR_INVALID_ARG;
+  if (!(scale > 0.0f) || !(scale < 3.0e38f)) return SVG_ERR_INVALID_ARG;
+  const size_t bytes = static_cast<size_t>(B) * H * Lq * c.d * 2;
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+  if (q0 < o0 + bytes && o0 < q0 + bytes) return SVG_ERR_INVALID_ARG;  // overlap
+  if (workspace_bytes < svg::prefix_workspace_bytes(c, B, H, Lq)) return SVG_ERR_CAPACITY;
+  const void* state[6] = {q, k_pages, v_pages, o, table, lens};
+  const void* lists[1] = {seqs};
+  int* status = nullptr;
+  if ((st = cache_common(geom, &c, 1, state, 6, lists, 1, &status)) != SVG_OK) return st;
+  svg::PrefixArgs a{c,       B,     H,    Lq,   prefix_seq, prefix_len, scale, q, k_pages,
+                    v_pages, table, lens, seqs, o,          lse,        workspace};
+  return svg::launch_prefix_attention(a, status, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SVG_OK
+             : SVG_ERR_CUDA;
+}
+
 svg_status svg_get_device_status(svg_stream_t stream, int32_t* bits) {
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return SVG_ERR_CUDA;
   cudaError_t err;
@@ -740,6 +935,7 @@ svg_status svg_get_device_status(svg_stream_t stream, int32_t* bits) {
   if (bits != nullptr) *bits = value;
   if (value & svg::kDevErrTimeout) return SVG_ERR_DEVICE_TIMEOUT;
   if (value & svg::kDevErrBounds) return SVG_ERR_INVALID_ARG;
+  if (value & svg::kDevErrCapacity) return SVG_ERR_CAPACITY;
   return SVG_OK;
 }
 

@@ -183,6 +183,47 @@ cudaError_t launch_permute_rows(int32_t BH, int32_t N, int32_t D, const svg_bf16
                                 const int32_t* order, svg_bf16* y, bool scatter, int* status,
                                 cudaStream_t stream);
 
+// History cache (cache.cu): sizes of a validated svg_cache_geom.
+struct CacheDims {
+  int32_t n_pages, ps, H_kv, d, max_seqs, max_pages;
+  __host__ __device__ int32_t max_rows() const { return max_pages * ps; }  // of one sequence
+};
+cudaError_t launch_cache_reset(const CacheDims& c, int32_t* table, int32_t* lens, int32_t* refs,
+                               cudaStream_t stream);
+cudaError_t launch_cache_fork(const CacheDims& c, int32_t* table, int32_t* lens, int32_t* refs,
+                              const int32_t* src, const int32_t* dst, int32_t n, int* status,
+                              cudaStream_t stream);
+cudaError_t launch_cache_free(const CacheDims& c, int32_t* table, int32_t* lens, int32_t* refs,
+                              const int32_t* seqs, const int32_t* keep, int32_t n, int* status,
+                              cudaStream_t stream);
+cudaError_t launch_cache_reserve(const CacheDims& c, int32_t* table, int32_t* lens, int32_t* refs,
+                                 const int32_t* seqs, const int32_t* counts, int32_t n,
+                                 int32_t* plan, int* status, cudaStream_t stream);
+cudaError_t launch_cache_write(const CacheDims& c, const int32_t* table, const int32_t* seqs,
+                               const int32_t* plan, int32_t n, int32_t L, const svg_bf16* k_new,
+                               const svg_bf16* v_new, svg_bf16* k_pages, svg_bf16* v_pages,
+                               int* status, cudaStream_t stream);
+cudaError_t launch_cache_compact(const CacheDims& c, const int32_t* table, const int32_t* refs,
+                                 int32_t* table_out, int32_t* refs_out, int32_t* moves, int* status,
+                                 cudaStream_t stream);
+cudaError_t launch_cache_copy(const CacheDims& c, const int32_t* moves, int32_t max_moves,
+                              const svg_bf16* k_src, const svg_bf16* v_src, svg_bf16* k_dst,
+                              svg_bf16* v_dst, int* status, cudaStream_t stream);
+
+// Attention over a shared history and each sequence's own rows (prefix_attention.cu).
+struct PrefixArgs {
+  CacheDims c;
+  int32_t B, H, Lq, prefix_seq, prefix_len;
+  float scale;
+  const svg_bf16 *q, *k_pages, *v_pages;
+  const int32_t *table, *lens, *seqs;
+  svg_bf16* o;
+  float* lse;
+  void* workspace;
+};
+size_t prefix_workspace_bytes(const CacheDims& c, int32_t B, int32_t H, int32_t Lq);
+cudaError_t launch_prefix_attention(const PrefixArgs& a, int* status, cudaStream_t stream);
+
 cudaError_t launch_wait_selftest(long long limit_cycles, int* status, cudaStream_t stream);
 
 }  // namespace svg

@@ -15,6 +15,7 @@ namespace svg {
 enum : int {
   kDevErrTimeout = 1,   // a bounded wait ran out
   kDevErrBounds = 2,    // an index read from caller memory was out of range
+  kDevErrCapacity = 4,  // a history cache had no room for the rows asked for
 };
 
 // A bounded wait gives up after this many SM clock cycles (about 1 s at 2 GHz);

@@ -319,3 +319,94 @@ class SemanticSparseLayer:
     def forward(self, q, k, v, o, lse=None, stream=None) -> None:
         self.plan(q, k, v, stream)
         self.attend(q, k, v, o, lse, stream)
+
+
+class HistoryCache:
+    """Keys and values of the frames made so far, and attention over them.
+
+    A generator that makes a video chunk by chunk attends from each chunk to all
+    frames before it. This class owns the page pools of `n_layers` layers, the
+    page table they share and the workspaces (allocated with torch), and calls
+    the library in order on one stream:
+
+      reserve(seqs, counts)     room for a chunk's rows in every sequence of the batch
+      write(layer, k, v)        a layer's keys and values of the chunk (again at
+                                each denoising step: the rows are overwritten)
+      attend(layer, q, ...)     the chunk's queries over the shared history and
+                                each sequence's own rows
+      fork(src, dst)            continuations of one history, sharing its pages
+      free(seqs, keep)          a sequence dropped, or cut back to its first rows
+      compact()                 the pages in use moved to the front of the pools
+
+    seqs, counts, src, dst and keep are device int32 tensors; negative sequence
+    numbers are idle entries of a padded batch. One cache is used by one stream
+    at a time, by one captured graph at a time as well.
+    """
+
+    def __init__(self, n_layers: int, n_pages: int, page_size: int, H: int, H_kv: int, d: int,
+                 max_seqs: int, max_rows: int, batch: int, rows: int, scale=None, device="cuda"):
+        """max_rows: of one sequence; batch, rows: the most sequences and query
+        rows a sequence that one call of reserve, write or attend has."""
+        from . import CacheGeom, svg_cache_reset, svg_prefix_attention_workspace_bytes
+        self.geom = CacheGeom(n_pages, page_size, H_kv, d, max_seqs, -(-max_rows // page_size))
+        self.H = H
+        self.scale = float(d ** -0.5 if scale is None else scale)
+        dev = self.device = torch.device(device)
+        need = svg_prefix_attention_workspace_bytes(self.geom, batch, H, rows)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.table = torch.empty((max_seqs, self.geom.max_pages), **i32)
+        self.lens, self.refs = torch.empty(max_seqs, **i32), torch.empty(n_pages, **i32)
+        self.plan = torch.empty((batch, 4), **i32)
+        self.moves = torch.empty(2 + 2 * n_pages, **i32)
+        shape = (n_pages, H_kv, page_size, d)
+        mk = lambda: torch.empty(shape, dtype=torch.bfloat16, device=dev)  # noqa: E731
+        self.pools = [(mk(), mk()) for _ in range(n_layers)]
+        self._seqs = None
+        svg_cache_reset(self.geom, self.table, self.lens, self.refs)
+
+    @property
+    def _state(self):
+        return self.table, self.lens, self.refs
+
+    def reset(self, stream=None) -> None:
+        from . import svg_cache_reset
+        svg_cache_reset(self.geom, *self._state, stream=stream)
+
+    def fork(self, src, dst, stream=None) -> None:
+        from . import svg_cache_fork
+        svg_cache_fork(self.geom, *self._state, src, dst, stream=stream)
+
+    def free(self, seqs, keep=None, stream=None) -> None:
+        from . import svg_cache_free
+        svg_cache_free(self.geom, *self._state, seqs, keep, stream=stream)
+
+    def reserve(self, seqs, counts, stream=None) -> None:
+        from . import svg_cache_reserve
+        svg_cache_reserve(self.geom, *self._state, seqs, counts, self.plan, stream=stream)
+        self._seqs = seqs
+
+    def write(self, layer: int, k_new, v_new, stream=None) -> None:
+        """k_new, v_new [n, H_kv, L, d]: the rows that the last reserve made room for."""
+        from . import svg_cache_write
+        if self._seqs is None:
+            raise ValueError("write follows reserve")
+        svg_cache_write(self.geom, self.table, self._seqs, self.plan, k_new.shape[2], k_new, v_new,
+                        *self.pools[layer], stream=stream)
+
+    def compact(self, stream=None) -> None:
+        from . import svg_cache_compact, svg_cache_copy_pages
+        svg_cache_compact(self.geom, self.table, self.refs, self.table, self.refs, self.moves,
+                          stream=stream)
+        for k, v in self.pools:
+            svg_cache_copy_pages(self.geom, self.moves, self.geom.n_pages, k, v, k, v,
+                                 stream=stream)
+        self._seqs = None  # the plan names pages by their old numbers
+
+    def attend(self, layer: int, q, seqs, prefix_seq: int, prefix_len: int, o, lse=None,
+               stream=None) -> None:
+        """q, o [B, H, Lq, d]; the first prefix_len rows of prefix_seq are shared by all."""
+        from . import svg_prefix_attention
+        svg_prefix_attention(self.geom, q.shape[0], self.H, q.shape[2], prefix_seq, prefix_len,
+                             self.scale, q, *self.pools[layer], self.table, self.lens, seqs, o,
+                             lse, self.workspace, stream=stream)
