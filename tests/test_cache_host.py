@@ -87,7 +87,7 @@ def test_list_lengths_and_shapes_are_refused(svg):
     assert call("svg_cache_write", _4=0) == svg.SVG_ERR_INVALID_ARG
     for n in (0, 9):
         assert call("svg_cache_copy_pages", _1=n) == svg.SVG_ERR_INVALID_ARG
-    for at in (dict(_0=0), dict(_0=2049), dict(_1=3), dict(_1=0), dict(_2=0), dict(_2=1 << 30),
+    for at in (dict(_0=0), dict(_0=1025), dict(_1=3), dict(_1=0), dict(_2=0), dict(_2=1 << 30),
                dict(_3=-1), dict(_3=4), dict(_4=-1), dict(_4=81),
                dict(_5=ctypes.c_float(0.0)), dict(_5=ctypes.c_float(float("nan"))),
                dict(_5=ctypes.c_float(float("inf"))),

@@ -148,7 +148,7 @@ CASES = {
     "tiles_cross_sequences": (7, 6, 2, 64, 16, 411, 31, [31, 40, 0, 1, 500, 128, 127]),
     "long_tails": (2, 2, 1, 64, 16, 16, 1, [5000, 3]),
     "batch_300": (300, 2, 1, 64, 16, 200, 1, [i % 41 for i in range(300)]),
-    "batch_2048": (2048, 1, 1, 64, 16, 33, 1, [i % 3 for i in range(2048)]),
+    "batch_1024": (1024, 1, 1, 64, 16, 33, 1, [i % 3 for i in range(1024)]),
     "one_sequence": (1, 8, 2, 128, 64, 1000, 5, [5]),
     "heads_40": (2, 40, 40, 64, 16, 90, 1, [3, 20]),
 }

@@ -876,7 +876,7 @@ static svg_status check_prefix_shape(const svg_cache_geom* geom, svg::CacheDims*
                                      int32_t H, int32_t Lq) {
   const svg_status st = check_cache(geom, c);
   if (st != SVG_OK) return st;
-  if (B < 1 || B > 2048 || H < 1 || Lq < 1 || H % c->H_kv != 0) return SVG_ERR_INVALID_ARG;
+  if (B < 1 || B > 1024 || H < 1 || Lq < 1 || H % c->H_kv != 0) return SVG_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * H > 0x7fffffffLL / Lq) return SVG_ERR_INVALID_ARG;
   return SVG_OK;
 }
