@@ -52,6 +52,10 @@ constexpr int kBK = 128;             // keys of a block
 constexpr int kGroup = 256;          // rows of an item
 constexpr int kMaxCtas = 148;
 constexpr int kMaxBatch = 1024;
+constexpr int kFewRows = 16;    // rows of an item of the few-row kernel
+constexpr int kFewWarps = 4;
+constexpr int kFewPerSm = 3;    // its CTAs per SM
+constexpr int kFewCtas = kMaxCtas * kFewPerSm;
 // Cost of a block: a two-tile block keeps the tensor core and the exponentials
 // busy for about 3.7k cycles, a one-tile block takes about as long as its
 // 64 KB take from HBM on every SM at once, 2.8k.
@@ -60,17 +64,30 @@ constexpr int kCostTwo = 4, kCostOne = 3;
 struct Sizes {
   int32_t n_ctas;   // CTAs launched
   int32_t B, H_kv, GL;
-  int32_t joint;    // 1: no shared items, the prefix belongs to every sequence's items
+  int32_t group;    // most rows of an item
+  int32_t shared, own;           // which items there are
+  int32_t joint;    // 1: no shared items, the prefix belongs to every sequence's own items
   int32_t prefix_len, nbp;       // blocks of the prefix
   int32_t groups_p, groups_s;    // row groups of a shared item's key head, of a sequence
   int32_t cost_p, cost_s;        // cost of one block over all those groups
 };
 
-__host__ __device__ inline int rows_of(int total, int g) {
-  const int r = total - g * kGroup;
-  return r < kGroup ? r : kGroup;
+__host__ __device__ inline int rows_of(int total, int g, int group) {
+  const int r = total - g * group;
+  return r < group ? r : group;
 }
 __host__ __device__ inline int cost_of(int rows) { return rows > 128 ? kCostTwo : kCostOne; }
+
+// Where the pieces of one kind of items (shared or own) go.
+struct Pieces {
+  int2* info;       // [items] first CTA and number of pieces
+  float* first_o;   // pieces with an item's first block: by q row, or (joint) by CTA and row
+  float2* first_ml;
+  float* head_o;    // [n_ctas][stride][d] piece of the item that began in an earlier CTA
+  float2* head_ml;
+  int32_t stride;   // rows of a CTA's place: the group size
+  int32_t groups;   // row groups of a key head (shared) or of a sequence (own)
+};
 
 struct __align__(64) Params {
   CUtensorMap tm_k, tm_v;
@@ -78,18 +95,14 @@ struct __align__(64) Params {
   Sizes z;
   int32_t prefix_seq;
   float scale_log2;
-  const svg_bf16* q;
+  const svg_bf16 *q, *k_pages, *v_pages;
   const int32_t *table, *lens, *seqs;
   svg_bf16* o;
   float* lse;
   int* status;
   // workspace
-  int32_t* head_item;  // [n_ctas] item that the CTA's piece begins inside of, or -1
-  int2* info;          // [items] first CTA and number of pieces
-  float* head_o;       // [n_ctas][256][d] piece of the item that began in an earlier CTA
-  float2* head_ml;
-  float* first_o;      // joint: [n_ctas][256][d]; else [2][rows][d] (shared, own) by q row
-  float2* first_ml;
+  int32_t* head_item;  // joint: [n_ctas] item that the CTA's piece begins inside of, or -1
+  Pieces part[2];      // shared, own
 };
 
 struct Barriers {
@@ -134,10 +147,10 @@ __device__ __forceinline__ bool prefix_ok(const CacheDims& c, const int32_t* len
   const int len = lens[seq];
   return len >= prefix_len && len <= c.max_rows();
 }
-// Blocks of a sequence's rows after the prefix; block numbers count from row 0
-// of the sequence, so the first one may begin before the prefix ends.
-__host__ __device__ inline int own_blocks(int len, int prefix_len) {
-  return len > prefix_len ? (len + kBK - 1) / kBK - prefix_len / kBK : 0;
+// Blocks of `bk` keys of a sequence's rows after the prefix; block numbers count
+// from row 0 of the sequence, so the first one may begin before the prefix ends.
+__host__ __device__ inline int own_blocks(int len, int prefix_len, int bk) {
+  return len > prefix_len ? (len + bk - 1) / bk - prefix_len / bk : 0;
 }
 
 // A piece of an item: blocks [lo, hi) of its nb.
@@ -158,7 +171,7 @@ struct Walk {
   __host__ __device__ Walk(const Sizes& sizes, const int64_t* cum_, int64_t from_, int64_t to_)
       : z(sizes), cum(cum_), from(from_), to(to_) {
     const int64_t per = static_cast<int64_t>(z.nbp) * z.cost_p;
-    const int64_t all = z.joint ? 0 : per * z.H_kv;
+    const int64_t all = z.shared ? per * z.H_kv : 0;
     int64_t rest = from;
     b = 0;
     if (rest < all) {
@@ -198,9 +211,8 @@ struct Walk {
       it.b = b;
       it.g = g;
       it.nb = shared ? z.nbp : static_cast<int>(cum[b + 1] - cum[b]);
-      it.rows = rows_of(shared ? z.B * z.GL : z.GL, g);
-      it.id = shared ? kv * z.groups_p + g
-                     : (z.joint ? 0 : z.H_kv * z.groups_p) + (kv * z.B + b) * z.groups_s + g;
+      it.rows = rows_of(shared ? z.B * z.GL : z.GL, g, z.group);
+      it.id = shared ? kv * z.groups_p + g : (kv * z.B + b) * z.groups_s + g;
       const int w = cost_of(it.rows);
       const int64_t begin = at;
       at += static_cast<int64_t>(it.nb) * w;
@@ -227,11 +239,12 @@ struct Walk {
   }
 };
 
-// Where block k of an item lies: block number `blk` of sequence `seq`, of whose
-// 128 keys [lo, hi) count.
+// Where block k (of BK keys) of an item lies: block number `blk` of sequence
+// `seq`, of whose keys [lo, hi) count.
 struct Block {
   int seq, blk, lo, hi;
 };
+template <int BK>
 __device__ __forceinline__ Block block_of(const Sizes& z, int prefix_seq, const int* s_seq,
                                           const int* s_len, const Item& it, int k) {
   Block r;
@@ -240,25 +253,89 @@ __device__ __forceinline__ Block block_of(const Sizes& z, int prefix_seq, const 
     r.seq = prefix_seq;
     r.blk = k;
     r.lo = 0;
-    r.hi = min(kBK, z.prefix_len - k * kBK);
+    r.hi = min(BK, z.prefix_len - k * BK);
   } else {
     r.seq = s_seq[it.b];
-    r.blk = k - pre + z.prefix_len / kBK;
-    r.lo = max(0, z.prefix_len - r.blk * kBK);
-    r.hi = min(kBK, s_len[it.b] - r.blk * kBK);
+    r.blk = k - pre + z.prefix_len / BK;
+    r.lo = max(0, z.prefix_len - r.blk * BK);
+    r.hi = min(BK, s_len[it.b] - r.blk * BK);
   }
   return r;
 }
 
 // q row (and o, lse row) of row r of an item.
 __device__ __forceinline__ int64_t q_row(const Sizes& z, const Item& it, int r) {
-  r += it.g * kGroup;
+  r += it.g * z.group;
   int b = it.b;
   if (it.shared) {
     b = r / z.GL;
     r -= b * z.GL;
   }
   return (static_cast<int64_t>(b) * z.H_kv + it.kv) * z.GL + r;
+}
+
+// The batch's lengths into shared memory and this CTA's piece [from, to) of the
+// line of cost; false: it has none. Every CTA finds the same line.
+template <int T, int BK>
+__device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int* s_seq, int* s_len,
+                                           int64_t& from, int64_t& to, int64_t& total,
+                                           int& n_pieces) {
+  const Sizes& z = p.z;
+  const int tid = threadIdx.x, cta = blockIdx.x;
+  const bool ok_prefix = prefix_ok(p.c, p.lens, p.prefix_seq, z.prefix_len);
+  for (int b = tid; b < z.B; b += T) {
+    const int seq = p.seqs[b];
+    const int len = entry_len(p.c, p.lens, seq);
+    if (cta == 0 && (len == -2 || !ok_prefix)) atomicOr(p.status, kDevErrBounds);
+    s_seq[b] = seq;
+    s_len[b] = len;
+    s_cum[b + 1] = len < 0 || !ok_prefix || !z.own
+                       ? 0
+                       : own_blocks(len, z.prefix_len, BK) + (z.joint ? z.nbp : 0);
+  }
+  __syncthreads();
+  if (tid < 32) {
+    int64_t sum = 0;
+    for (int b0 = 0; b0 < z.B; b0 += 32) {
+      int64_t x = b0 + tid < z.B ? s_cum[b0 + tid + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (tid >= o) x += y;
+      }
+      x += sum;
+      if (b0 + tid < z.B) s_cum[b0 + tid + 1] = x;
+      sum = __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (tid == 0) s_cum[0] = 0;
+  }
+  __syncthreads();
+  total = s_cum[z.B] * z.cost_s * z.H_kv;
+  if (z.shared && ok_prefix) total += static_cast<int64_t>(z.nbp) * z.cost_p * z.H_kv;
+  // No piece is smaller than a block, so that every CTA from an item's first to
+  // its last has a piece of it.
+  const int64_t most = total / kCostTwo < 1 ? 1 : total / kCostTwo;
+  n_pieces = static_cast<int>(most < z.n_ctas ? most : z.n_ctas);
+  if (cta >= n_pieces || total == 0) return false;
+  from = total * cta / n_pieces;
+  to = total * (cta + 1) / n_pieces;
+  return true;
+}
+
+// First CTA (this one) and number of pieces of the item whose first block it has.
+__device__ __forceinline__ int2 pieces_of(const Item& it, int64_t end, int64_t total, int n_pieces) {
+  const int w = cost_of(it.rows);
+  const int64_t x = end - w;  // where the last block begins
+  int64_t last = x * n_pieces / total;
+  while (total * (last + 1) / n_pieces <= x) ++last;
+  return make_int2(blockIdx.x, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1);
+}
+
+// Where row rr of an item's piece goes.
+__device__ __forceinline__ int64_t piece_place(const Params& p, const Item& it, int rr, int64_t row) {
+  if (it.lo > 0 || p.z.joint)
+    return static_cast<int64_t>(blockIdx.x) * p.part[it.shared ? 0 : 1].stride + rr;
+  return row;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -285,45 +362,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5;
   const int cta = blockIdx.x;
 
-  // ---- the batch's lengths, and this CTA's piece of the work
-  const bool ok_prefix = prefix_ok(p.c, p.lens, p.prefix_seq, z.prefix_len);
-  for (int b = tid; b < z.B; b += kThreads) {
-    const int seq = p.seqs[b];
-    const int len = entry_len(p.c, p.lens, seq);
-    if (cta == 0 && (len == -2 || !ok_prefix)) atomicOr(p.status, kDevErrBounds);
-    s_seq[b] = seq;
-    s_len[b] = len;
-    s_cum[b + 1] = len < 0 || !ok_prefix ? 0
-                                         : own_blocks(len, z.prefix_len) + (z.joint ? z.nbp : 0);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int64_t sum = 0;
-    for (int b0 = 0; b0 < z.B; b0 += 32) {
-      int64_t x = b0 + tid < z.B ? s_cum[b0 + tid + 1] : 0;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (tid >= o) x += y;
-      }
-      x += sum;
-      if (b0 + tid < z.B) s_cum[b0 + tid + 1] = x;
-      sum = __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (tid == 0) s_cum[0] = 0;
-  }
-  __syncthreads();
-  int64_t total = s_cum[z.B] * z.cost_s * z.H_kv;
-  if (!z.joint && ok_prefix) total += static_cast<int64_t>(z.nbp) * z.cost_p * z.H_kv;
-  // No piece is smaller than a block, so that every CTA from an item's first to
-  // its last has a piece of it.
-  const int64_t most = total / kCostTwo < 1 ? 1 : total / kCostTwo;
-  const int n_pieces = static_cast<int>(most < z.n_ctas ? most : z.n_ctas);
-  if (cta >= n_pieces || total == 0) {
-    if (tid == 0) p.head_item[cta] = -1;
+  int64_t from, to, total;
+  int n_pieces;
+  if (!plan_piece<kThreads, kBK>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) {
+    if (z.joint && tid == 0) p.head_item[cta] = -1;
     return;
   }
-  const int64_t from = total * cta / n_pieces, to = total * (cta + 1) / n_pieces;
 
   // ---- barriers and tensor memory
   if (warp == 0) {
@@ -381,14 +425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int n = 0;  // blocks issued
       bool ok = true;
       while (ok && walk.next(it)) {
-        Block blk = block_of(z, p.prefix_seq, s_seq, s_len, it, it.lo);
+        Block blk = block_of<kBK>(z, p.prefix_seq, s_seq, s_len, it, it.lo);
         int page = page_of(blk);
         for (int k = it.lo; k < it.hi; ++k, ++n) {
           const int y = page < 0 ? past
                                  : (page * p.c.H_kv + it.kv) * p.c.ps +
                                        (blk.blk * kBK + bx * box) % p.c.ps;
           if (k + 1 < it.hi) {  // the next block's pages, while this one waits
-            blk = block_of(z, p.prefix_seq, s_seq, s_len, it, k + 1);
+            blk = block_of<kBK>(z, p.prefix_seq, s_seq, s_len, it, k + 1);
             page = page_of(blk);
           }
           const int st = n % C::kStages;
@@ -559,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n0 = 0, sc = 0, ones = 0;
     uint32_t fp = 0;  // bit t: parity of the next final commit of tile t
     bool ok = true;
-    if (tid == 0) p.head_item[cta] = -1;
+    if (z.joint && tid == 0) p.head_item[cta] = -1;
     while (ok && walk.next(it)) {
       const int n = it.hi - it.lo;
       const bool two = it.rows > 128;
@@ -567,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool active = (warp & 3) * 32 < rows;  // warp-uniform
       float m = -INFINITY, l = 0.0f;                // log2 units
       for (int j = two ? 0 : t; j < n; j += two ? 1 : 2, ++sc) {
-        const Block blk = block_of(z, p.prefix_seq, s_seq, s_len, it, it.lo + j);
+        const Block blk = block_of<kBK>(z, p.prefix_seq, s_seq, s_len, it, it.lo + j);
         const bool ragged = blk.lo > 0 || blk.hi < kBK;
         ok = mbar_wait(&bar->s_full[t], sc & 1, abort_flag, p.status);
         if (!ok) break;
@@ -689,20 +733,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rr = two ? t * 128 + r : r;  // row of the item
       const bool valid = r < rows;
       const int64_t row = valid ? q_row(z, it, rr) : 0;
-      const int64_t slot = static_cast<int64_t>(cta) * kGroup + rr;
-      float* out = nullptr;
-      float2* out_ml = nullptr;
-      if (it.lo > 0) {
-        out = p.head_o + slot * D;
-        out_ml = p.head_ml + slot;
-      } else if (z.joint) {
-        out = p.first_o + slot * D;
-        out_ml = p.first_ml + slot;
-      } else {
-        const int64_t at = row + (it.shared ? 0 : static_cast<int64_t>(z.B) * z.H_kv * z.GL);
-        out = p.first_o + at * D;
-        out_ml = p.first_ml + at;
-      }
+      const Pieces& part = p.part[it.shared ? 0 : 1];
+      const int64_t place = piece_place(p, it, rr, row);
+      float* out = (it.lo > 0 ? part.head_o : part.first_o) + place * D;
+      float2* out_ml = (it.lo > 0 ? part.head_ml : part.first_ml) + place;
       const float inv_l = l > 0.0f ? 1.0f / l : 0.0f;
       // two tiles: all columns of this tile's O; one tile: this warpgroup's half of both
       const int c_lo = two ? 0 : t * (D / 2), c_n = two ? D : D / 2;
@@ -758,14 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tid == 0) {
         if (it.lo > 0) {
-          p.head_item[cta] = it.id;
+          if (z.joint) p.head_item[cta] = it.id;
         } else if (!final_rows) {
-          // the CTA that has the item's last block
-          const int64_t begin = walk.at - static_cast<int64_t>(it.nb) * cost_of(it.rows);
-          const int64_t x = begin + static_cast<int64_t>(it.nb - 1) * cost_of(it.rows);
-          int64_t last = x * n_pieces / total;
-          while (total * (last + 1) / n_pieces <= x) ++last;
-          p.info[it.id] = make_int2(cta, static_cast<int>(last) - cta + 1);
+          part.info[it.id] = pieces_of(it, walk.at, total, n_pieces);
         }
       }
       n0 += n;
@@ -778,6 +807,300 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// Items of up to 16 rows: one row of a few sequences over a long prefix, or one
+// sequence's rows over its own keys. The products are too small for a
+// 128-row tensor-memory tile to pay (its softmax keeps one warp busy and its
+// per-item hand-overs cost more than a tail of a few hundred keys), and what bounds
+// the work is reading K and V once. So each warp streams 16 keys (32 at d = 64)
+// from global memory straight into the registers of mma.sync m16n8k16 operands,
+// with 16-byte loads and no shared memory between:
+//   S = Q K^T   the B operand wants pairs along d of one key: lane (g, c) loads
+//               dims (4j + c) 8 .. + 8 of key g. Which d is which k of the
+//               product is free as long as Q's operand uses the same order.
+//   O += P V    the B operand wants pairs along the keys of one column: lane (g, c)
+//               loads dims 8g .. 8g + 8 of keys 2c, 2c+1, 2c+8, 2c+9 and
+//               interleaves them; column g of product t is channel 8g + t.
+// The next step's K is loaded when this step's S is done, its V after O.
+// A CTA's four warps take the steps of a piece in turn and are joined
+// in shared memory at its end.
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {  // read once: not kept in L1
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <int D>
+struct FewCfg {
+  static constexpr int kKeys = 2048 / D;        // keys of a warp's step
+  static constexpr int kUnit = kKeys * kFewWarps;  // keys of a CTA's step: the block of the line
+  static constexpr int kOffQ = 0;               // uint4 [D/32][2][32]: Q in operand order
+  static constexpr int kOffO = kOffQ + D / 32 * 2 * 32 * 16;  // float [warps][16][D]
+  static constexpr int kOffMl = kOffO + kFewWarps * kFewRows * D * 4;
+  static constexpr int kOffBatch = kOffMl + kFewWarps * kFewRows * 8;
+  static constexpr int smem(int B) { return kOffBatch + (B + 1) * 8 + 2 * B * 4; }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
+    prefix_few_kernel(const __grid_constant__ Params p) {
+  using C = FewCfg<D>;
+  constexpr int kThreadsFew = kFewWarps * 32;
+  constexpr int NG = C::kKeys / 16;  // groups of 16 keys (one page each) of a step
+  constexpr int NJ = D / 32;         // 16-byte chunks a lane has of a K row
+  constexpr int NH = D / 64;         // and of a V row
+  extern __shared__ __align__(16) uint8_t few_smem[];
+  uint4* s_q = reinterpret_cast<uint4*>(few_smem + C::kOffQ);
+  float* s_o = reinterpret_cast<float*>(few_smem + C::kOffO);
+  float2* s_ml = reinterpret_cast<float2*>(few_smem + C::kOffMl);
+  const Sizes& z = p.z;
+  int64_t* s_cum = reinterpret_cast<int64_t*>(few_smem + C::kOffBatch);
+  int* s_seq = reinterpret_cast<int*>(s_cum + z.B + 1);
+  int* s_len = s_seq + z.B;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
+  const int g = lane >> 2, c = lane & 3;
+
+  int64_t from, to, total;
+  int n_pieces;
+  if (!plan_piece<kThreadsFew, C::kUnit>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) return;
+  Walk walk(z, s_cum, from, to);
+  Item it;
+  while (walk.next(it)) {
+    // ---- Q in operand order; rows past the item's are zeros
+    __syncthreads();
+    for (int i = tid; i < NJ * 2 * 32; i += kThreadsFew) {
+      const int r = (i >> 2 & 7) + (i >> 5 & 1) * 8, ch = (i >> 6) * 4 + (i & 3);
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (r < it.rows) x = reinterpret_cast<const uint4*>(p.q + q_row(z, it, r) * D)[ch];
+      s_q[(i >> 6) * 64 + (i >> 5 & 1) * 32 + (i & 31)] = x;
+    }
+    __syncthreads();
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows g and g + 8, log2 units
+
+    // The step of block k: its first key's position and the positions that count.
+    struct Step {
+      int key0, lo, hi;
+      int64_t base[NG];  // row of the pool of each 16 keys; -1: zeros
+    };
+    auto step_of = [&](int k) {
+      const Block b = block_of<C::kUnit>(z, p.prefix_seq, s_seq, s_len, it, k);
+      Step s;
+      s.key0 = b.blk * C::kUnit + warp * C::kKeys;
+      s.lo = b.blk * C::kUnit + b.lo;
+      s.hi = b.blk * C::kUnit + b.hi;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const int pos = s.key0 + n * 16;
+        s.base[n] = -1;
+        if (pos < s.hi && pos + 16 > s.lo) {
+          const int page =
+              __ldg(p.table + static_cast<int64_t>(b.seq) * p.c.max_pages + pos / p.c.ps);
+          if (page >= 0 && page < p.c.n_pages) {
+            s.base[n] = (static_cast<int64_t>(page) * p.c.H_kv + it.kv) * p.c.ps + pos % p.c.ps;
+          } else if (lane == 0) {
+            atomicOr(p.status, kDevErrBounds);
+          }
+        }
+      }
+      return s;
+    };
+    uint4 kx[NG][2][NJ], vx[NG][4][NH];
+    auto load_k = [&](const Step& s) {
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = n * 16 + u * 8 + g;
+          const bool in = s.base[n] >= 0 && s.key0 + key >= s.lo && s.key0 + key < s.hi;
+          const uint4* src =
+              reinterpret_cast<const uint4*>(p.k_pages + (s.base[n] + u * 8 + g) * D) + c;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            kx[n][u][j] = in ? ld_stream(src + j * 4) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto load_v = [&](const Step& s) {
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = 2 * c + (i & 1) + (i >> 1) * 8;
+          const int key = n * 16 + at;
+          const bool in = s.base[n] >= 0 && s.key0 + key >= s.lo && s.key0 + key < s.hi;
+          const uint4* src = reinterpret_cast<const uint4*>(p.v_pages + (s.base[n] + at) * D) + g;
+#pragma unroll
+          for (int h = 0; h < NH; ++h)
+            vx[n][i][h] = in ? ld_stream(src + h * 8) : make_uint4(0, 0, 0, 0);
+        }
+    };
+
+    Step cur = step_of(it.lo);
+    load_k(cur);
+    load_v(cur);
+    for (int k = it.lo; k < it.hi; ++k) {
+      const bool more = k + 1 < it.hi;
+      Step nxt = cur;
+      if (more) nxt = step_of(k + 1);
+      float s[NG][2][4];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][u][e] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const uint4 qa = s_q[j * 64 + lane], qb = s_q[j * 64 + 32 + lane];
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            mma_16816(s[n][u], qa.x, qb.x, qa.y, qb.y, kx[n][u][j].x, kx[n][u][j].y);
+            mma_16816(s[n][u], qa.z, qb.z, qa.w, qb.w, kx[n][u][j].z, kx[n][u][j].w);
+          }
+      }
+      if (more) load_k(nxt);
+      if (cur.key0 < cur.lo || cur.key0 + C::kKeys > cur.hi) {
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int pos = cur.key0 + n * 16 + u * 8 + 2 * c + (e & 1);
+              if (pos < cur.lo || pos >= cur.hi) s[n][u][e] = -INFINITY;
+            }
+      }
+      // ---- running maximum and sum of rows g (e = 0, 1) and g + 8 (e = 2, 3)
+      float alpha[2], base[2];
+      bool rebase = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) x = fmax3(x, s[n][u][2 * r], s[n][u][2 * r + 1]);
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2)) * p.scale_log2;
+        const bool up = x > m[r] + kRebaseLog2;
+        alpha[r] = up ? fast_exp2(m[r] - x) : 1.0f;
+        m[r] = up ? x : m[r];
+        base[r] = m[r] == -INFINITY ? 0.0f : m[r];
+        rebase = rebase || up;
+        l[r] *= alpha[r];
+      }
+      if (__any_sync(0xffffffffu, rebase)) {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e >> 1];
+      }
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        uint32_t pa[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float e0 = fast_exp2(fmaf(s[n][u][2 * r], p.scale_log2, -base[r]));
+            const float e1 = fast_exp2(fmaf(s[n][u][2 * r + 1], p.scale_log2, -base[r]));
+            l[r] += e0 + e1;
+            pa[u * 2 + r] = pack_bf16x2(e0, e1);
+          }
+#pragma unroll
+        for (int h = 0; h < NH; ++h) {
+          const uint4 &v0 = vx[n][0][h], &v1 = vx[n][1][h], &v2 = vx[n][2][h], &v3 = vx[n][3][h];
+          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+          const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const uint32_t pick = t & 1 ? 0x7632u : 0x5410u;
+            mma_16816(o[h * 8 + t], pa[0], pa[1], pa[2], pa[3],
+                      __byte_perm(w0[t >> 1], w1[t >> 1], pick),
+                      __byte_perm(w2[t >> 1], w3[t >> 1], pick));
+          }
+        }
+      }
+      if (more) load_v(nxt);
+      cur = nxt;
+    }
+
+    // ---- the four warps' (O, m, l) joined
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (c == 0) s_ml[warp * kFewRows + g + 8 * r] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    float f[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, s_ml[w * kFewRows + g + 8 * r].x);
+      f[r] = fast_exp2(m[r] - (top == -INFINITY ? 0.0f : top));
+    }
+    // a lane has channels 8 (8h + 2c) .. + 16 of its rows
+#pragma unroll
+    for (int h = 0; h < NH; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (g + 8 * (e >> 1) >= it.rows) continue;
+        float* dst = s_o + (warp * kFewRows + g + 8 * (e >> 1)) * D + (h * 8 + 2 * c + (e & 1)) * 8;
+#pragma unroll
+        for (int t = 0; t < 8; t += 4)
+          *reinterpret_cast<float4*>(dst + t) =
+              make_float4(o[h * 8 + t][e] * f[e >> 1], o[h * 8 + t + 1][e] * f[e >> 1],
+                          o[h * 8 + t + 2][e] * f[e >> 1], o[h * 8 + t + 3][e] * f[e >> 1]);
+      }
+    __syncthreads();
+    const Pieces& part = p.part[it.shared ? 0 : 1];
+    float* out = it.lo > 0 ? part.head_o : part.first_o;
+    float2* out_ml = it.lo > 0 ? part.head_ml : part.first_ml;
+    for (int i = tid; i < it.rows * (D / 4); i += kThreadsFew) {
+      const int r = i / (D / 4), ch = i % (D / 4);
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kFewWarps; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(s_o + (w * kFewRows + r) * D + ch * 4);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      const int64_t place = piece_place(p, it, r, q_row(z, it, r));
+      *reinterpret_cast<float4*>(out + place * D + ch * 4) = x;
+      if (ch == 0) {
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, s_ml[w * kFewRows + r].x);
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w)
+          sum += s_ml[w * kFewRows + r].y *
+                 fast_exp2(s_ml[w * kFewRows + r].x - (top == -INFINITY ? 0.0f : top));
+        out_ml[place] = make_float2(top, sum);
+      }
+    }
+    if (tid == 0 && it.lo == 0) part.info[it.id] = pieces_of(it, walk.at, total, n_pieces);
   }
 }
 
@@ -832,19 +1155,17 @@ __global__ void __launch_bounds__(W * 32) join_rows_kernel(const __grid_constant
 #pragma unroll
   for (int e = 0; e < kE; ++e) o[e] = 0.0f;
   Joined s{-INFINITY, 0.0f};
-  for (int part = 0; part < 2; ++part) {  // the shared item's pieces, then the own one's
-    const int in_item = part == 0 ? b * z.GL + rr : rr;
-    if ((part == 0 ? z.nbp : own_blocks(len, z.prefix_len)) == 0) continue;
-    const int g = in_item / kGroup;
-    const int2 info = p.info[part == 0 ? kv * z.groups_p + g
-                                       : z.H_kv * z.groups_p + (kv * z.B + b) * z.groups_s + g];
-    const int64_t first = row + (part == 0 ? 0 : static_cast<int64_t>(z.B) * z.H_kv * z.GL);
-    const int64_t head = static_cast<int64_t>(info.x) * kGroup + in_item % kGroup;
+  for (int i = 0; i < 2; ++i) {  // the shared item's pieces, then the own one's
+    if ((i == 0 ? z.prefix_len : len - z.prefix_len) <= 0) continue;
+    const Pieces& part = p.part[i];
+    const int in_item = i == 0 ? b * z.GL + rr : rr;
+    const int2 info = part.info[(i == 0 ? kv : kv * z.B + b) * part.groups + in_item / part.stride];
+    const int64_t head = static_cast<int64_t>(info.x) * part.stride + in_item % part.stride;
 #pragma unroll 4
-    for (int i = warp; i < info.y; i += W) {
-      const int64_t at = i == 0 ? first : head + static_cast<int64_t>(i) * kGroup;
-      join_one<D>(o, s, (i == 0 ? p.first_o : p.head_o) + at * D,
-                  (i == 0 ? p.first_ml : p.head_ml)[at]);
+    for (int k = warp; k < info.y; k += W) {
+      const int64_t at = k == 0 ? row : head + static_cast<int64_t>(k) * part.stride;
+      join_one<D>(o, s, (k == 0 ? part.first_o : part.head_o) + at * D,
+                  (k == 0 ? part.first_ml : part.head_ml)[at]);
     }
   }
   if (W > 1) {
@@ -884,7 +1205,8 @@ __global__ void __launch_bounds__(256) join_cuts_kernel(const __grid_constant__ 
   const int cta = blockIdx.x;
   const int id = p.head_item[cta];
   if (id < 0) return;
-  const int2 info = p.info[id];
+  const Pieces& part = p.part[1];
+  const int2 info = part.info[id];
   if (info.x != cta - 1) return;  // an earlier cut's block has it
   Item it;
   it.shared = 0;
@@ -892,50 +1214,97 @@ __global__ void __launch_bounds__(256) join_cuts_kernel(const __grid_constant__ 
   it.b = id / z.groups_s % z.B;
   it.kv = id / z.groups_s / z.B;
   const int r = blockIdx.y * 8 + warp;
-  if (r >= rows_of(z.GL, it.g)) return;
+  if (r >= rows_of(z.GL, it.g, z.group)) return;
   int64_t at = static_cast<int64_t>(info.x) * kGroup + r;
-  join_one<D>(o, s, p.first_o + at * D, p.first_ml[at]);
+  join_one<D>(o, s, part.first_o + at * D, part.first_ml[at]);
   for (int i = 1; i < info.y; ++i) {
     at += kGroup;
-    join_one<D>(o, s, p.head_o + at * D, p.head_ml[at]);
+    join_one<D>(o, s, part.head_o + at * D, part.head_ml[at]);
   }
   store_row<D>(p, q_row(z, it, r), o, s);
 }
 
-inline int groups(int rows) { return (rows + kGroup - 1) / kGroup; }
-inline int group_cost(int rows) {
-  const int g = groups(rows);
-  return (g - 1) * kCostTwo + cost_of(rows_of(rows, g - 1));
+inline int groups(int rows, int group) { return (rows + group - 1) / group; }
+inline int group_cost(int rows, int group) {
+  const int g = groups(rows, group);
+  return (g - 1) * kCostTwo + cost_of(rows_of(rows, g - 1, group));
 }
 
-// Whether the rows of one sequence fill the row groups so well that gathering
-// all sequences' rows over the prefix saves less than a tenth of it.
-inline bool joint_by_rows(int B, int GL) {
-  return 10.0 * group_cost(B * GL) > 9.0 * static_cast<double>(B) * group_cost(GL);
+// Which kernel has which items. Rows of one sequence up to 16: its own keys go to
+// the few-row kernel, and the prefix too if all sequences' rows are up
+// to 16. Otherwise joint items, unless gathering all sequences' rows over the
+// prefix saves a tenth of it or more.
+enum Form { kFew, kMixed, kGathered, kJoint };
+inline Form form_of(int B, int GL, bool prefix) {
+  if (GL <= kFewRows) return B * GL <= kFewRows || !prefix ? kFew : kMixed;
+  if (!prefix) return kJoint;
+  return 10.0 * group_cost(B * GL, kGroup) > 9.0 * static_cast<double>(B) * group_cost(GL, kGroup)
+             ? kJoint
+             : kGathered;
 }
 
-struct Layout {
-  size_t info, head_o, head_ml, first_o, first_ml, bytes;
+struct Place {
+  size_t info, first_o, first_ml, head_o, head_ml;
 };
-Layout layout(const CacheDims& c, int32_t B, int32_t H, int32_t Lq, bool joint) {
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+struct Layout {
+  Place part[2];
+  size_t head_item, bytes;
+};
+Layout layout(const CacheDims& c, int32_t B, int32_t H, int32_t Lq, Form form) {
   const int GL = H / c.H_kv * Lq;
-  const size_t items = static_cast<size_t>(c.H_kv) * B * groups(GL) +
-                       (joint ? 0 : static_cast<size_t>(c.H_kv) * groups(B * GL));
-  const size_t slots = static_cast<size_t>(kMaxCtas) * kGroup;
-  const size_t firsts = joint ? slots : 2 * static_cast<size_t>(B) * H * Lq;
+  const size_t rows = static_cast<size_t>(B) * H * Lq;
   Layout l;
-  l.info = up(kMaxCtas * sizeof(int32_t));
-  l.head_o = up(l.info + items * sizeof(int2));
-  l.head_ml = up(l.head_o + slots * c.d * sizeof(float));
-  l.first_o = up(l.head_ml + slots * sizeof(float2));
-  l.first_ml = up(l.first_o + firsts * c.d * sizeof(float));
-  l.bytes = up(l.first_ml + firsts * sizeof(float2));
+  memset(&l, 0, sizeof(l));
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += (n + 255) / 256 * 256;
+    return here;
+  };
+  l.head_item = take(kMaxCtas * sizeof(int32_t));
+  for (int i = 0; i < 2; ++i) {
+    if (form == kJoint && i == 0) continue;
+    const bool few = form == kFew || (form == kMixed && i == 1);
+    const int group = few ? kFewRows : kGroup;
+    const size_t slots = few ? kFewCtas * kFewRows : kMaxCtas * kGroup;
+    const size_t items = i == 0 ? static_cast<size_t>(c.H_kv) * groups(B * GL, group)
+                                : static_cast<size_t>(c.H_kv) * B * groups(GL, group);
+    const size_t firsts = form == kJoint ? slots : rows;
+    l.part[i].info = take(items * sizeof(int2));
+    l.part[i].first_o = take(firsts * c.d * sizeof(float));
+    l.part[i].first_ml = take(firsts * sizeof(float2));
+    l.part[i].head_o = take(slots * c.d * sizeof(float));
+    l.part[i].head_ml = take(slots * sizeof(float2));
+  }
+  l.bytes = at;
   return l;
 }
 
+// The sizes of the line of one kernel: `few` of them in blocks and groups.
+Sizes sizes_of(const PrefixArgs& a, int n_ctas, bool few, bool shared, bool own, bool joint) {
+  const int GL = a.H / a.c.H_kv * a.Lq;
+  const int bk = few ? kFewWarps * 2048 / a.c.d : kBK, group = few ? kFewRows : kGroup;
+  Sizes z;
+  memset(&z, 0, sizeof(z));
+  z.n_ctas = n_ctas;
+  z.B = a.B;
+  z.H_kv = a.c.H_kv;
+  z.GL = GL;
+  z.group = group;
+  z.shared = shared && a.prefix_len > 0;
+  z.own = own;
+  z.joint = joint;
+  z.prefix_len = a.prefix_len;
+  z.nbp = (a.prefix_len + bk - 1) / bk;
+  z.groups_p = groups(a.B * GL, group);
+  z.groups_s = groups(GL, group);
+  z.cost_p = group_cost(a.B * GL, group);
+  z.cost_s = group_cost(GL, group);
+  return z;
+}
+
 template <int D>
-cudaError_t launch(const Params& p, int64_t rows, cudaStream_t stream) {
+cudaError_t launch_tiles(const Params& p, cudaStream_t stream) {
   using C = Cfg<D>;
   auto kern = prefix_attention_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -945,10 +1314,35 @@ cudaError_t launch(const Params& p, int64_t rows, cudaStream_t stream) {
   if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
   if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
   kern<<<p.z.n_ctas, kThreads, C::kSmem, stream>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  if (p.z.joint) {
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_few(const Params& p, cudaStream_t stream) {
+  using C = FewCfg<D>;
+  auto kern = prefix_few_kernel<D>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::smem(kMaxBatch));
+  if (e != cudaSuccess) return e;
+  kern<<<p.z.n_ctas, kFewWarps * 32, C::smem(p.z.B), stream>>>(p);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const PrefixArgs& a, Params& p, Form form, int sms, cudaStream_t stream) {
+  cudaError_t e = cudaSuccess;
+  if (form == kFew || form == kMixed) {
+    p.z = sizes_of(a, sms * kFewPerSm, true, form == kFew, true, false);
+    if ((e = launch_few<D>(p, stream)) != cudaSuccess) return e;
+  }
+  if (form != kFew) {
+    p.z = sizes_of(a, sms, false, form != kJoint, form != kMixed, form == kJoint);
+    if ((e = launch_tiles<D>(p, stream)) != cudaSuccess) return e;
+  }
+  if (form == kJoint) {
     join_cuts_kernel<D><<<dim3(p.z.n_ctas, kGroup / 8), 256, 0, stream>>>(p);
   } else {
+    const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.Lq;
     join_rows_kernel<D, 4><<<static_cast<unsigned>(rows), 128, 0, stream>>>(p);
   }
   return cudaGetLastError();
@@ -957,58 +1351,56 @@ cudaError_t launch(const Params& p, int64_t rows, cudaStream_t stream) {
 }  // namespace
 
 size_t prefix_workspace_bytes(const CacheDims& c, int32_t B, int32_t H, int32_t Lq) {
-  size_t n = layout(c, B, H, Lq, true).bytes;
-  if (!joint_by_rows(B, H / c.H_kv * Lq)) {
-    const size_t m = layout(c, B, H, Lq, false).bytes;
-    if (m > n) n = m;
-  }
-  return n;
+  const int GL = H / c.H_kv * Lq;
+  const size_t with = layout(c, B, H, Lq, form_of(B, GL, true)).bytes;
+  const size_t without = layout(c, B, H, Lq, form_of(B, GL, false)).bytes;
+  return with > without ? with : without;
 }
 
 cudaError_t launch_prefix_attention(const PrefixArgs& a, int* status, cudaStream_t stream) {
   Params p;
   memset(&p, 0, sizeof(p));
-  const int32_t pool_rows = a.c.n_pages * a.c.H_kv * a.c.ps;
-  const int box = a.c.ps < kBK ? a.c.ps : kBK;
-  if (!make_tmap_bf16(&p.tm_k, a.k_pages, a.c.d, pool_rows, 1, box) ||
-      !make_tmap_bf16(&p.tm_v, a.v_pages, a.c.d, pool_rows, 1, box))
-    return cudaErrorInvalidValue;
+  const int GL = a.H / a.c.H_kv * a.Lq;
+  const Form form = form_of(a.B, GL, a.prefix_len > 0);
+  if (form != kFew) {
+    const int32_t pool_rows = a.c.n_pages * a.c.H_kv * a.c.ps;
+    const int box = a.c.ps < kBK ? a.c.ps : kBK;
+    if (!make_tmap_bf16(&p.tm_k, a.k_pages, a.c.d, pool_rows, 1, box) ||
+        !make_tmap_bf16(&p.tm_v, a.v_pages, a.c.d, pool_rows, 1, box))
+      return cudaErrorInvalidValue;
+  }
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const int GL = a.H / a.c.H_kv * a.Lq;
+  if (sms > kMaxCtas) sms = kMaxCtas;
   p.c = a.c;
-  p.z.n_ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  p.z.B = a.B;
-  p.z.H_kv = a.c.H_kv;
-  p.z.GL = GL;
-  p.z.joint = a.prefix_len == 0 || joint_by_rows(a.B, GL) ? 1 : 0;
-  p.z.prefix_len = a.prefix_len;
-  p.z.nbp = (a.prefix_len + kBK - 1) / kBK;
-  p.z.groups_p = groups(a.B * GL);
-  p.z.groups_s = groups(GL);
-  p.z.cost_p = group_cost(a.B * GL);
-  p.z.cost_s = group_cost(GL);
   p.prefix_seq = a.prefix_seq;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.q = a.q;
+  p.k_pages = a.k_pages;
+  p.v_pages = a.v_pages;
   p.table = a.table;
   p.lens = a.lens;
   p.seqs = a.seqs;
   p.o = a.o;
   p.lse = a.lse;
   p.status = status;
-  const Layout l = layout(a.c, a.B, a.H, a.Lq, p.z.joint != 0);
+  const Layout l = layout(a.c, a.B, a.H, a.Lq, form);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  p.head_item = reinterpret_cast<int32_t*>(ws);
-  p.info = reinterpret_cast<int2*>(ws + l.info);
-  p.head_o = reinterpret_cast<float*>(ws + l.head_o);
-  p.head_ml = reinterpret_cast<float2*>(ws + l.head_ml);
-  p.first_o = reinterpret_cast<float*>(ws + l.first_o);
-  p.first_ml = reinterpret_cast<float2*>(ws + l.first_ml);
-  const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.Lq;
-  return a.c.d == 128 ? launch<128>(p, rows, stream) : launch<64>(p, rows, stream);
+  p.head_item = reinterpret_cast<int32_t*>(ws + l.head_item);
+  for (int i = 0; i < 2; ++i) {
+    const bool few = form == kFew || (form == kMixed && i == 1);
+    Pieces& t = p.part[i];
+    t.info = reinterpret_cast<int2*>(ws + l.part[i].info);
+    t.first_o = reinterpret_cast<float*>(ws + l.part[i].first_o);
+    t.first_ml = reinterpret_cast<float2*>(ws + l.part[i].first_ml);
+    t.head_o = reinterpret_cast<float*>(ws + l.part[i].head_o);
+    t.head_ml = reinterpret_cast<float2*>(ws + l.part[i].head_ml);
+    t.stride = few ? kFewRows : kGroup;
+    t.groups = groups(i == 0 ? a.B * GL : GL, t.stride);
+  }
+  return a.c.d == 128 ? launch<128>(a, p, form, sms, stream) : launch<64>(a, p, form, sms, stream);
 }
 
 }  // namespace svg
