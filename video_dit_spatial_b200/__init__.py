@@ -377,90 +377,125 @@ def svg2_sparse_attention(BH, N, d, block_k, scale, qs, ks, vs, row_ptr, col_idx
 # ---------------------------------------------------------------------------
 # history cache and the attention that reads it
 # ---------------------------------------------------------------------------
-def _buf(name: str, x, dtype: str, numel: int) -> Optional[int]:
+_torch = None
+
+
+def _here():
+    """torch and the current device's index, for the checks below."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    if not _torch.cuda.is_initialized() and not _torch.cuda.is_available():
+        return _torch, -2  # no device: no tensor passes the checks
+    return _torch, _torch.cuda.current_device()
+
+
+def _buf(name: str, x, dtype, numel: int, dev: int) -> Optional[int]:
     """Device address of a buffer of the history cache: as _ptr, and a tensor
     must be on the current device, of the given type and large enough (the
     kernels take sizes from the geometry, not from the tensor)."""
-    ptr = _ptr(x)
-    if x is None or isinstance(x, int):
-        return ptr
-    import torch
-    if x.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {x.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
-    if x.dtype != getattr(torch, dtype):
+    if x is None or x.__class__ is int:
+        return x
+    if (x.get_device() == dev and x.dtype is dtype and x.numel() >= numel and x.is_contiguous()):
+        return x.data_ptr()
+    _ptr(x)  # names a host tensor or a strided view
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, the current device is cuda:{dev}")
+    if x.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.numel() < numel:
-        raise ValueError(f"{name} needs {numel} values, got {x.numel()}")
-    return ptr
+    raise ValueError(f"{name} needs {numel} values, got {x.numel()}")
 
 
-def _state(geom: CacheGeom, table, lens, refs):
-    return (_buf("table", table, "int32", geom.max_seqs * geom.max_pages),
-            _buf("lens", lens, "int32", geom.max_seqs),
-            _buf("refs", refs, "int32", geom.n_pages))
+def _stream_on(dev: int, stream) -> Optional[int]:
+    """As _stream; the current stream's handle without making a Stream object
+    (0.1 us instead of 3 us, which is as much as the rest of a short call)."""
+    if stream is None and dev >= 0:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return _stream(stream)
 
 
-def _pool(geom: CacheGeom, **pages):
+def _state(geom: CacheGeom, table, lens, refs, i32, dev: int):
+    return (_buf("table", table, i32, geom.max_seqs * geom.max_pages, dev),
+            _buf("lens", lens, i32, geom.max_seqs, dev),
+            _buf("refs", refs, i32, geom.n_pages, dev))
+
+
+def _pool(geom: CacheGeom, bf16, dev: int, **pages):
     n = geom.n_pages * geom.H_kv * geom.page_size * geom.head_dim
-    return [_buf(name, x, "bfloat16", n) for name, x in pages.items()]
+    return [_buf(name, x, bf16, n, dev) for name, x in pages.items()]
 
 
 def svg_cache_reset(geom: CacheGeom, table, lens, refs, stream=None) -> None:
+    torch, dev = _here()
     _check("svg_cache_reset", load().svg_cache_reset(
-        ctypes.byref(geom), *_state(geom, table, lens, refs), _stream(stream)))
+        ctypes.byref(geom), *_state(geom, table, lens, refs, torch.int32, dev),
+        _stream_on(dev, stream)))
 
 
 def svg_cache_fork(geom: CacheGeom, table, lens, refs, src, dst, n=None, stream=None) -> None:
+    torch, dev = _here()
+    i32 = torch.int32
     n = src.numel() if n is None else n
     _check("svg_cache_fork", load().svg_cache_fork(
-        ctypes.byref(geom), *_state(geom, table, lens, refs), _buf("src", src, "int32", n),
-        _buf("dst", dst, "int32", n), n, _stream(stream)))
+        ctypes.byref(geom), *_state(geom, table, lens, refs, i32, dev),
+        _buf("src", src, i32, n, dev), _buf("dst", dst, i32, n, dev), n, _stream_on(dev, stream)))
 
 
 def svg_cache_free(geom: CacheGeom, table, lens, refs, seqs, keep=None, n=None,
                    stream=None) -> None:
+    torch, dev = _here()
+    i32 = torch.int32
     n = seqs.numel() if n is None else n
     _check("svg_cache_free", load().svg_cache_free(
-        ctypes.byref(geom), *_state(geom, table, lens, refs), _buf("seqs", seqs, "int32", n),
-        _buf("keep", keep, "int32", n), n, _stream(stream)))
+        ctypes.byref(geom), *_state(geom, table, lens, refs, i32, dev),
+        _buf("seqs", seqs, i32, n, dev), _buf("keep", keep, i32, n, dev), n,
+        _stream_on(dev, stream)))
 
 
 def svg_cache_reserve(geom: CacheGeom, table, lens, refs, seqs, counts, plan, n=None,
                       stream=None) -> None:
+    torch, dev = _here()
+    i32 = torch.int32
     n = seqs.numel() if n is None else n
     _check("svg_cache_reserve", load().svg_cache_reserve(
-        ctypes.byref(geom), *_state(geom, table, lens, refs), _buf("seqs", seqs, "int32", n),
-        _buf("counts", counts, "int32", n), n, _buf("plan", plan, "int32", 4 * n),
-        _stream(stream)))
+        ctypes.byref(geom), *_state(geom, table, lens, refs, i32, dev),
+        _buf("seqs", seqs, i32, n, dev), _buf("counts", counts, i32, n, dev), n,
+        _buf("plan", plan, i32, 4 * n, dev), _stream_on(dev, stream)))
 
 
 def svg_cache_write(geom: CacheGeom, table, seqs, plan, L, k_new, v_new, k_pages, v_pages,
                     n=None, stream=None) -> None:
+    torch, dev = _here()
+    i32, bf16 = torch.int32, torch.bfloat16
     n = seqs.numel() if n is None else n
     rows = n * geom.H_kv * L * geom.head_dim
     _check("svg_cache_write", load().svg_cache_write(
-        ctypes.byref(geom), _buf("table", table, "int32", geom.max_seqs * geom.max_pages),
-        _buf("seqs", seqs, "int32", n), _buf("plan", plan, "int32", 4 * n), n, L,
-        _buf("k_new", k_new, "bfloat16", rows), _buf("v_new", v_new, "bfloat16", rows),
-        *_pool(geom, k_pages=k_pages, v_pages=v_pages), _stream(stream)))
+        ctypes.byref(geom), _buf("table", table, i32, geom.max_seqs * geom.max_pages, dev),
+        _buf("seqs", seqs, i32, n, dev), _buf("plan", plan, i32, 4 * n, dev), n, L,
+        _buf("k_new", k_new, bf16, rows, dev), _buf("v_new", v_new, bf16, rows, dev),
+        *_pool(geom, bf16, dev, k_pages=k_pages, v_pages=v_pages), _stream_on(dev, stream)))
 
 
 def svg_cache_compact(geom: CacheGeom, table, refs, table_out, refs_out, moves,
                       stream=None) -> None:
-    entries = geom.max_seqs * geom.max_pages
+    torch, dev = _here()
+    i32, entries = torch.int32, geom.max_seqs * geom.max_pages
     _check("svg_cache_compact", load().svg_cache_compact(
-        ctypes.byref(geom), _buf("table", table, "int32", entries),
-        _buf("refs", refs, "int32", geom.n_pages), _buf("table_out", table_out, "int32", entries),
-        _buf("refs_out", refs_out, "int32", geom.n_pages),
-        _buf("moves", moves, "int32", 2 + 2 * geom.n_pages), _stream(stream)))
+        ctypes.byref(geom), _buf("table", table, i32, entries, dev),
+        _buf("refs", refs, i32, geom.n_pages, dev),
+        _buf("table_out", table_out, i32, entries, dev),
+        _buf("refs_out", refs_out, i32, geom.n_pages, dev),
+        _buf("moves", moves, i32, 2 + 2 * geom.n_pages, dev), _stream_on(dev, stream)))
 
 
 def svg_cache_copy_pages(geom: CacheGeom, moves, max_moves, k_src, v_src, k_dst, v_dst,
                          stream=None) -> None:
+    torch, dev = _here()
     _check("svg_cache_copy_pages", load().svg_cache_copy_pages(
-        ctypes.byref(geom), _buf("moves", moves, "int32", 2 + 2 * max_moves), max_moves,
-        *_pool(geom, k_src=k_src, v_src=v_src, k_dst=k_dst, v_dst=v_dst), _stream(stream)))
+        ctypes.byref(geom), _buf("moves", moves, torch.int32, 2 + 2 * max_moves, dev), max_moves,
+        *_pool(geom, torch.bfloat16, dev, k_src=k_src, v_src=v_src, k_dst=k_dst, v_dst=v_dst),
+        _stream_on(dev, stream)))
 
 
 def svg_prefix_attention_workspace_bytes(geom: CacheGeom, B: int, H: int, Lq: int) -> int:
@@ -473,13 +508,16 @@ def svg_prefix_attention_workspace_bytes(geom: CacheGeom, B: int, H: int, Lq: in
 def svg_prefix_attention(geom: CacheGeom, B, H, Lq, prefix_seq, prefix_len, scale, q, k_pages,
                          v_pages, table, lens, seqs, o, lse, workspace, workspace_bytes=None,
                          stream=None) -> None:
-    rows = B * H * Lq
+    torch, dev = _here()
+    i32, bf16, rows = torch.int32, torch.bfloat16, B * H * Lq
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
+    ws = _buf("workspace", workspace, workspace.dtype, 0, dev) \
+        if workspace.__class__ is not int else workspace
     _check("svg_prefix_attention", load().svg_prefix_attention(
         ctypes.byref(geom), B, H, Lq, prefix_seq, prefix_len, scale,
-        _buf("q", q, "bfloat16", rows * geom.head_dim),
-        *_pool(geom, k_pages=k_pages, v_pages=v_pages),
-        _buf("table", table, "int32", geom.max_seqs * geom.max_pages),
-        _buf("lens", lens, "int32", geom.max_seqs), _buf("seqs", seqs, "int32", B),
-        _buf("o", o, "bfloat16", rows * geom.head_dim), _buf("lse", lse, "float32", rows),
-        _ptr(workspace), wb, _stream(stream)))
+        _buf("q", q, bf16, rows * geom.head_dim, dev),
+        *_pool(geom, bf16, dev, k_pages=k_pages, v_pages=v_pages),
+        _buf("table", table, i32, geom.max_seqs * geom.max_pages, dev),
+        _buf("lens", lens, i32, geom.max_seqs, dev), _buf("seqs", seqs, i32, B, dev),
+        _buf("o", o, bf16, rows * geom.head_dim, dev), _buf("lse", lse, torch.float32, rows, dev),
+        ws, wb, _stream_on(dev, stream)))

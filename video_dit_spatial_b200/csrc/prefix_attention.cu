@@ -21,8 +21,10 @@
 // fp32 and joined by a second kernel.
 //
 // One CTA per SM walks its piece. 384 threads: warps 0-3 and 4-7 softmax
-// and epilogue (thread = row = tensor-memory lane), warp 8 TMA producer, warp 9
-// MMA issuer, warps 10-11 load query rows. Two forms of an item:
+// and epilogue (thread = row = tensor-memory lane), warp 8 loads K, warp 9 issues
+// the products, warp 10 loads V, warp 11 query rows (K and V apart, since a V
+// buffer is free only after its softmax, and the K after it must not wait for that).
+// Two forms of an item:
 //   two tiles  129..256 rows: tile A and tile B, each block serves both;
 //   one tile   up to 128 rows: tile A and tile B hold the SAME rows, A takes
 //              the even blocks and B the odd ones, so that one's softmax
@@ -40,9 +42,9 @@ namespace svg {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kProducerWarp = 8;
+constexpr int kKWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr int kLoadThreads = 64;  // warps 10 and 11
+constexpr int kVWarp = 10;
 constexpr int kLaunchRegs = 168;
 constexpr int kSoftmaxRegs = 224;
 constexpr int kOtherRegs = 56;
@@ -78,19 +80,23 @@ __host__ __device__ inline int rows_of(int total, int g, int group) {
 }
 __host__ __device__ inline int cost_of(int rows) { return rows > 128 ? kCostTwo : kCostOne; }
 
-// Where the pieces of one kind of items (shared or own) go.
+// Where the pieces of one kind of items (shared or own) go: a slot holds
+// `stride` rows, row r's channels 4c .. 4c + 3 as a float4 at r * rs + c * cs. The tile
+// kernel, with a row per lane, writes slots channel by channel (rs = 1), the
+// few-row kernel row by row (cs = 1), so that either writes whole lines.
 struct Pieces {
   int2* info;       // [items] first CTA and number of pieces
-  float* first_o;   // pieces with an item's first block: by q row, or (joint) by CTA and row
+  float4* first_o;  // pieces with an item's first block: a slot per item, or (joint) per CTA
   float2* first_ml;
-  float* head_o;    // [n_ctas][stride][d] piece of the item that began in an earlier CTA
+  float4* head_o;   // piece of the item that began in an earlier CTA: a slot per CTA
   float2* head_ml;
-  int32_t stride;   // rows of a CTA's place: the group size
-  int32_t groups;   // row groups of a key head (shared) or of a sequence (own)
+  int32_t stride, rs, cs;
+  int32_t group;    // rows of an item at most
+  int32_t groups;   // items of a key head (shared) or of a sequence and key head (own)
 };
 
 struct __align__(64) Params {
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_k, tm_v, tm_q;  // tm_q: the rows of q, for items of one sequence
   CacheDims c;
   Sizes z;
   int32_t prefix_seq;
@@ -166,7 +172,7 @@ struct Walk {
   int shared, kv, b, g;
 
   __host__ __device__ __forceinline__ int64_t own_cost() const {
-    return cum[z.B] * z.cost_s;
+    return z.own ? cum[z.B] * z.cost_s : 0;
   }
   __host__ __device__ Walk(const Sizes& sizes, const int64_t* cum_, int64_t from_, int64_t to_)
       : z(sizes), cum(cum_), from(from_), to(to_) {
@@ -205,7 +211,7 @@ struct Walk {
     }
   }
   __host__ __device__ bool next(Item& it) {
-    while (at < to && (shared || kv < z.H_kv)) {
+    while (at < to && (shared || (z.own && kv < z.H_kv))) {
       it.shared = shared;
       it.kv = kv;
       it.b = b;
@@ -274,6 +280,19 @@ __device__ __forceinline__ int64_t q_row(const Sizes& z, const Item& it, int r) 
   return (static_cast<int64_t>(b) * z.H_kv + it.kv) * z.GL + r;
 }
 
+// No piece is smaller than a block, so that every CTA from an item's first to
+// its last has a piece of it.
+__device__ __forceinline__ bool cut_piece(const Sizes& z, int64_t total, int64_t& from, int64_t& to,
+                                          int& n_pieces) {
+  const int64_t most = total / kCostTwo < 1 ? 1 : total / kCostTwo;
+  n_pieces = static_cast<int>(most < z.n_ctas ? most : z.n_ctas);
+  const int cta = blockIdx.x;
+  if (cta >= n_pieces || total == 0) return false;
+  from = total * cta / n_pieces;
+  to = total * (cta + 1) / n_pieces;
+  return true;
+}
+
 // The batch's lengths into shared memory and this CTA's piece [from, to) of the
 // line of cost; false: it has none. Every CTA finds the same line.
 template <int T, int BK>
@@ -283,13 +302,17 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
   const Sizes& z = p.z;
   const int tid = threadIdx.x, cta = blockIdx.x;
   const bool ok_prefix = prefix_ok(p.c, p.lens, p.prefix_seq, z.prefix_len);
+  if (!z.own) {  // no sequence's own keys: the shared items alone
+    total = ok_prefix ? static_cast<int64_t>(z.nbp) * z.cost_p * z.H_kv : 0;
+    return cut_piece(z, total, from, to, n_pieces);
+  }
   for (int b = tid; b < z.B; b += T) {
     const int seq = p.seqs[b];
     const int len = entry_len(p.c, p.lens, seq);
     if (cta == 0 && (len == -2 || !ok_prefix)) atomicOr(p.status, kDevErrBounds);
     s_seq[b] = seq;
     s_len[b] = len;
-    s_cum[b + 1] = len < 0 || !ok_prefix || !z.own
+    s_cum[b + 1] = len < 0 || !ok_prefix
                        ? 0
                        : own_blocks(len, z.prefix_len, BK) + (z.joint ? z.nbp : 0);
   }
@@ -312,14 +335,7 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
   __syncthreads();
   total = s_cum[z.B] * z.cost_s * z.H_kv;
   if (z.shared && ok_prefix) total += static_cast<int64_t>(z.nbp) * z.cost_p * z.H_kv;
-  // No piece is smaller than a block, so that every CTA from an item's first to
-  // its last has a piece of it.
-  const int64_t most = total / kCostTwo < 1 ? 1 : total / kCostTwo;
-  n_pieces = static_cast<int>(most < z.n_ctas ? most : z.n_ctas);
-  if (cta >= n_pieces || total == 0) return false;
-  from = total * cta / n_pieces;
-  to = total * (cta + 1) / n_pieces;
-  return true;
+  return cut_piece(z, total, from, to, n_pieces);
 }
 
 // First CTA (this one) and number of pieces of the item whose first block it has.
@@ -331,11 +347,9 @@ __device__ __forceinline__ int2 pieces_of(const Item& it, int64_t end, int64_t t
   return make_int2(blockIdx.x, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1);
 }
 
-// Where row rr of an item's piece goes.
-__device__ __forceinline__ int64_t piece_place(const Params& p, const Item& it, int rr, int64_t row) {
-  if (it.lo > 0 || p.z.joint)
-    return static_cast<int64_t>(blockIdx.x) * p.part[it.shared ? 0 : 1].stride + rr;
-  return row;
+// Slot of an item's piece in this CTA's hands.
+__device__ __forceinline__ int64_t slot_of(const Params& p, const Item& it) {
+  return it.lo > 0 || p.z.joint ? blockIdx.x : it.id;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -361,6 +375,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Sizes& z = p.z;
   const int tid = threadIdx.x, warp = tid >> 5;
   const int cta = blockIdx.x;
+  if (tid == 0) {
+    prefetch_tensormap(&p.tm_k);
+    prefetch_tensormap(&p.tm_v);
+    prefetch_tensormap(&p.tm_q);
+  }
 
   int64_t from, to, total;
   int n_pieces;
@@ -377,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 32) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar->q_full[s], kLoadThreads);
+      mbar_init(&bar->q_full[s], 32);
       mbar_init(&bar->q_empty[s], 1);
       mbar_init(&bar->s_full[s], 1);
       mbar_init(&bar->p_full[s], 128);
@@ -403,11 +422,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   Item it;
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == kProducerWarp) {
-      // ---------------------------------------------------------- producer
+    if (warp == kKWarp || warp == kVWarp) {
+      // ---------------------------------------------------------- K or V
       // A block is 128 / box boxes of min(page_size, 128) rows, times the panels;
       // a lane loads one of them. Boxes without a row that counts and pages
       // past the pool are read from past the end of the map: zeros.
+      const bool is_k = warp == kKWarp;
+      uint64_t* full = is_k ? bar->k_full : bar->v_full;
+      uint64_t* empty = is_k ? bar->k_empty : bar->v_empty;
+      const CUtensorMap* map = is_k ? &p.tm_k : &p.tm_v;
+      uint8_t* ring = is_k ? sK : sV;
       const int lane = lane_id();
       const int box = min(p.c.ps, kBK);
       const int boxes = kBK / box;
@@ -436,38 +460,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             page = page_of(blk);
           }
           const int st = n % C::kStages;
-          const uint32_t par = ((n / C::kStages) & 1) ^ 1;
           if (lane == 0) {
-            ok = mbar_wait(&bar->k_empty[st], par, abort_flag, p.status);
-            if (ok) mbar_arrive_expect_tx(&bar->k_full[st], C::kTile);
+            ok = mbar_wait(&empty[st], ((n / C::kStages) & 1) ^ 1, abort_flag, p.status);
+            if (ok) mbar_arrive_expect_tx(&full[st], C::kTile);
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           if (loads)
-            tma_load_3d(sK + st * C::kTile + pn * C::kPanel + bx * box * 128, &p.tm_k,
-                        &bar->k_full[st], pn * 64, y, 0);
-          if (lane == 0) {
-            ok = mbar_wait(&bar->v_empty[st], par, abort_flag, p.status);
-            if (ok) mbar_arrive_expect_tx(&bar->v_full[st], C::kTile);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) {
-            ++n;  // the keys of this block are on their way
-            break;
-          }
-          if (loads)
-            tma_load_3d(sV + st * C::kTile + pn * C::kPanel + bx * box * 128, &p.tm_v,
-                        &bar->v_full[st], pn * 64, y, 0);
+            tma_load_3d(ring + st * C::kTile + pn * C::kPanel + bx * box * 128, map, &full[st],
+                        pn * 64, y, 0);
         }
       }
       if (!ok && lane == 0) {
-        // Let every copy this warp started land before the CTA retires; a
-        // barrier that nothing was posted on just runs into the limit.
+        // Let every copy this warp started land before the CTA retires.
         for (int j = (n > C::kStages ? n - C::kStages : 0); j < n; ++j) {
-          const int st = j % C::kStages;
-          const uint32_t par = (j / C::kStages) & 1;
           const long long t0 = clock64();
-          while (!(mbar_try_wait(&bar->k_full[st], par) && mbar_try_wait(&bar->v_full[st], par)) &&
+          while (!mbar_try_wait(&full[j % C::kStages], (j / C::kStages) & 1) &&
                  clock64() - t0 < kWaitLimitCycles) {
           }
         }
@@ -511,9 +519,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && walk.next(it)) {
           const int n = it.hi - it.lo;
           const bool two = it.rows > 128;
-          for (int t = 0; t < (two ? 2 : 1); ++t)
-            wait(&bar->q_full[(qn + t) & 1], ((qn + t) >> 1) & 1);
-          if (!ok) break;
           for (int j = 0; ok && j <= n; ++j) {
             const int st = (n0 + j) % C::kStages, par = ((n0 + j) / C::kStages) & 1;
             const int pst = (n0 + j - 1 + C::kStages) % C::kStages;
@@ -527,9 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if (!wait_p(t)) break;
                   tc_fence_after();
                   pv(t, pst, j == 1);
+                  if (t == 1) tc_commit(&bar->v_empty[pst]);
                   if (j == n) tc_commit(&bar->o_final[t]);
                 }
                 if (j < n) {
+                  if (j == 0 && !wait(&bar->q_full[(qn + t) & 1], ((qn + t) >> 1) & 1)) break;
                   if (t == 0 && !wait(&bar->k_full[st], par)) break;
                   tc_fence_after();
                   qk(t, (qn + t) & 1, st);
@@ -537,10 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
               if (!ok) break;
-              if (j > 0) tc_commit(&bar->v_empty[pst]);
               if (j < n) tc_commit(&bar->k_empty[st]);
             } else {
               if (j < n) {
+                if (j == 0 && !wait(&bar->q_full[qn & 1], (qn >> 1) & 1)) break;
                 if (!wait(&bar->k_full[st], par)) break;
                 tc_fence_after();
                 qk(j & 1, qn & 1, st);
@@ -572,24 +579,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ---------------------------------------------------------- query rows
-      const int lt = tid - (kMmaWarp + 1) * 32;
+      // The rows of one sequence are one run of q: a tiled load (what it brings of
+      // other rows past the item's end is never used). Gathered rows come by
+      // 16-byte copies to the same swizzled places.
+      const int lane = lane_id();
       constexpr int kVecs = D / 8;  // 16-byte vectors of a row
       const uint32_t q_addr = smem_u32(sQ);
-      const int vec = lt % kVecs;
+      const int vec = lane % kVecs;
       int qn = 0;
       bool ok = true;
       while (ok && walk.next(it)) {
         for (int r0 = 0; r0 < it.rows; r0 += 128, ++qn) {
+          uint64_t* full = &bar->q_full[qn & 1];
           ok = mbar_wait(&bar->q_empty[qn & 1], ((qn >> 1) & 1) ^ 1, abort_flag, p.status);
-          if (!ok) break;
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+          if (!it.shared) {
+            if (lane == 0) {
+              const int64_t row = q_row(z, it, r0);
+              mbar_arrive_expect_tx(full, C::kTile);
+              for (int pn = 0; pn < C::kPanels; ++pn)
+                tma_load_3d(sQ + (qn & 1) * C::kTile + pn * C::kPanel, &p.tm_q, full, pn * 64,
+                            static_cast<int>(row), 0);
+            } else {
+              mbar_arrive(full);
+            }
+            continue;
+          }
           const uint32_t dst = q_addr + (qn & 1) * C::kTile + (vec >> 3) * C::kPanel;
           const int rows = min(it.rows - r0, 128);
-          for (int r = lt / kVecs; r < rows; r += kLoadThreads / kVecs)
+#pragma unroll 8
+          for (int r = lane / kVecs; r < rows; r += 32 / kVecs)
             cp_async16(dst + r * 128 + (((vec & 7) ^ (r & 7)) << 4),
                        p.q + q_row(z, it, r0 + r) * D + vec * 8);
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();
-          mbar_arrive(&bar->q_full[qn & 1]);
+          mbar_arrive(full);
+        }
+      }
+      if (!ok && lane == 0) {
+        // Let the tiled loads this warp started land before the CTA retires.
+        for (int j = (qn > 2 ? qn - 2 : 0); j < qn; ++j) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(&bar->q_full[j & 1], (j >> 1) & 1) &&
+                 clock64() - t0 < kWaitLimitCycles) {
+          }
         }
       }
     }
@@ -734,9 +770,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = r < rows;
       const int64_t row = valid ? q_row(z, it, rr) : 0;
       const Pieces& part = p.part[it.shared ? 0 : 1];
-      const int64_t place = piece_place(p, it, rr, row);
-      float* out = (it.lo > 0 ? part.head_o : part.first_o) + place * D;
-      float2* out_ml = (it.lo > 0 ? part.head_ml : part.first_ml) + place;
+      const int64_t slot = slot_of(p, it) * part.stride;
+      float4* out = (it.lo > 0 ? part.head_o : part.first_o) + slot * (D / 4) + rr;
+      float2* out_ml = (it.lo > 0 ? part.head_ml : part.first_ml) + slot + rr;
       const float inv_l = l > 0.0f ? 1.0f / l : 0.0f;
       // two tiles: all columns of this tile's O; one tile: this warpgroup's half of both
       const int c_lo = two ? 0 : t * (D / 2), c_n = two ? D : D / 2;
@@ -774,10 +810,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               dst[v] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(out + c0);
+            float4* dst = out + static_cast<int64_t>(c0 / 4) * part.stride;
 #pragma unroll
             for (int v = 0; v < 8; ++v)
-              dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+              dst[v * part.stride] = make_float4(u2f(o[4 * v]), u2f(o[4 * v + 1]),
+                                                 u2f(o[4 * v + 2]), u2f(o[4 * v + 3]));
           }
         }
       }
@@ -1077,8 +1114,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
       }
     __syncthreads();
     const Pieces& part = p.part[it.shared ? 0 : 1];
-    float* out = it.lo > 0 ? part.head_o : part.first_o;
-    float2* out_ml = it.lo > 0 ? part.head_ml : part.first_ml;
+    const int64_t slot = slot_of(p, it) * part.stride;
+    float4* out = (it.lo > 0 ? part.head_o : part.first_o) + slot * (D / 4);
+    float2* out_ml = (it.lo > 0 ? part.head_ml : part.first_ml) + slot;
     for (int i = tid; i < it.rows * (D / 4); i += kThreadsFew) {
       const int r = i / (D / 4), ch = i % (D / 4);
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1087,8 +1125,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
         const float4 y = *reinterpret_cast<const float4*>(s_o + (w * kFewRows + r) * D + ch * 4);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }
-      const int64_t place = piece_place(p, it, r, q_row(z, it, r));
-      *reinterpret_cast<float4*>(out + place * D + ch * 4) = x;
+      out[i] = x;
       if (ch == 0) {
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -1097,7 +1134,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
         for (int w = 0; w < kFewWarps; ++w)
           sum += s_ml[w * kFewRows + r].y *
                  fast_exp2(s_ml[w * kFewRows + r].x - (top == -INFINITY ? 0.0f : top));
-        out_ml[place] = make_float2(top, sum);
+        out_ml[r] = make_float2(top, sum);
       }
     }
     if (tid == 0 && it.lo == 0) part.info[it.id] = pieces_of(it, walk.at, total, n_pieces);
@@ -1105,123 +1142,119 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
 }
 
 // ---------------------------------------------------------------- joining the pieces
-// A warp of the W that share a row takes every W-th piece, four at a time.
+// A block joins eight rows: lane (r, c) of warp w has row r's float4 number 4w + c,
+// which reads either layout of a slot in runs of 64 bytes or more. F warps take
+// turns at the pieces of the same channels.
 struct Joined {
   float m, l;
+  float4 o;
 };
-template <int D>
-__device__ __forceinline__ void join_one(float (&o)[D / 32], Joined& s, const float* src, float2 ml) {
-  constexpr int kE = D / 32;
-  float x[kE];
-  const int lane = lane_id();
-#pragma unroll
-  for (int e = 0; e < kE; ++e) x[e] = src[e * 32 + lane];
+
+__device__ __forceinline__ void join_one(Joined& s, float2 ml, float4 x) {
   const float m = fmaxf(s.m, ml.x);
   const float m_use = m == -INFINITY ? 0.0f : m;
   const float a = fast_exp2(s.m - m_use), b = fast_exp2(ml.x - m_use);
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = o[e] * a + (ml.x == -INFINITY ? 0.0f : x[e] * b);
+  if (ml.x == -INFINITY) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // no key: nothing was summed
+  s.o = make_float4(s.o.x * a + x.x * b, s.o.y * a + x.y * b, s.o.z * a + x.z * b,
+                    s.o.w * a + x.w * b);
   s.l = s.l * a + ml.y * b;
   s.m = m;
 }
 
 template <int D>
-__device__ __forceinline__ void store_row(const Params& p, int64_t row, const float (&o)[D / 32],
-                                          const Joined& s) {
+__device__ __forceinline__ void store_row(const Params& p, int64_t row, int c4, const Joined& s) {
   const float inv = s.l > 0.0f ? 1.0f / s.l : 0.0f;
-  const int lane = lane_id();
-#pragma unroll
-  for (int e = 0; e < D / 32; ++e)
-    p.o[row * D + e * 32 + lane] = static_cast<svg_bf16>(pack_bf16x2(o[e] * inv, 0.0f) & 0xffffu);
-  if (p.lse != nullptr && lane == 0)
+  *reinterpret_cast<uint2*>(p.o + row * D + c4 * 4) =
+      make_uint2(pack_bf16x2(s.o.x * inv, s.o.y * inv), pack_bf16x2(s.o.z * inv, s.o.w * inv));
+  if (p.lse != nullptr && c4 == 0)
     p.lse[row] = s.l > 0.0f ? (s.m + __log2f(s.l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Shared and own items: one row per block of W warps.
-template <int D, int W>
-__global__ void __launch_bounds__(W * 32) join_rows_kernel(const __grid_constant__ Params p) {
-  constexpr int kE = D / 32;
-  __shared__ float s_o[W][D];
-  __shared__ float2 s_ml[W];
-  const Sizes& z = p.z;
-  const int warp = threadIdx.x >> 5, lane = lane_id();
-  const int64_t row = blockIdx.x;
-  const int64_t bk = row / z.GL;
-  const int b = static_cast<int>(bk / z.H_kv), kv = static_cast<int>(bk % z.H_kv);
-  const int rr = static_cast<int>(row % z.GL);
-  const int len = entry_len(p.c, p.lens, p.seqs[b]);
-  if (len < 0 || !prefix_ok(p.c, p.lens, p.prefix_seq, z.prefix_len)) return;
-  float o[kE];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = 0.0f;
-  Joined s{-INFINITY, 0.0f};
-  for (int i = 0; i < 2; ++i) {  // the shared item's pieces, then the own one's
-    if ((i == 0 ? z.prefix_len : len - z.prefix_len) <= 0) continue;
-    const Pieces& part = p.part[i];
-    const int in_item = i == 0 ? b * z.GL + rr : rr;
-    const int2 info = part.info[(i == 0 ? kv : kv * z.B + b) * part.groups + in_item / part.stride];
-    const int64_t head = static_cast<int64_t>(info.x) * part.stride + in_item % part.stride;
+// Pieces k = first, first + step, ... of row r of an item.
+template <int D>
+__device__ __forceinline__ void join_pieces(Joined& s, const Pieces& part, int2 info,
+                                            int64_t first_slot, int r, int c4, int first, int step) {
 #pragma unroll 4
-    for (int k = warp; k < info.y; k += W) {
-      const int64_t at = k == 0 ? row : head + static_cast<int64_t>(k) * part.stride;
-      join_one<D>(o, s, (k == 0 ? part.first_o : part.head_o) + at * D,
-                  (k == 0 ? part.first_ml : part.head_ml)[at]);
+  for (int k = first; k < info.y; k += step) {
+    const int64_t slot = (k == 0 ? first_slot : info.x + k) * part.stride;
+    join_one(s, (k == 0 ? part.first_ml : part.head_ml)[slot + r],
+             (k == 0 ? part.first_o : part.head_o)[slot * (D / 4) + r * part.rs + c4 * part.cs]);
+  }
+}
+
+// Shared and own items.
+template <int D, int F>
+__global__ void __launch_bounds__(D * 2 * F) join_rows_kernel(const __grid_constant__ Params p) {
+  constexpr int kChunks = D / 16;  // warps that cover a row
+  __shared__ float4 s_o[F > 1 ? F - 1 : 1][kChunks * 32];
+  __shared__ float2 s_ml[F > 1 ? F - 1 : 1][kChunks * 32];
+  const Sizes& z = p.z;
+  const int lane = lane_id(), chunk = (threadIdx.x >> 5) % kChunks, f = (threadIdx.x >> 5) / kChunks;
+  const int64_t rows = static_cast<int64_t>(z.B) * z.H_kv * z.GL;
+  const int64_t row = blockIdx.x * static_cast<int64_t>(8) + (lane >> 2);
+  const int c4 = chunk * 4 + (lane & 3);
+  Joined s{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  bool live = row < rows;
+  if (live) {
+    const int64_t bk = row / z.GL;
+    const int rr = static_cast<int>(row - bk * z.GL);
+    const int b = static_cast<int>(bk / z.H_kv), kv = static_cast<int>(bk - static_cast<int64_t>(b) * z.H_kv);
+    const int len = entry_len(p.c, p.lens, p.seqs[b]);
+    live = len >= 0 && prefix_ok(p.c, p.lens, p.prefix_seq, z.prefix_len);
+    for (int i = 0; i < 2; ++i) {  // the shared item's pieces, then the own one's
+      if (!live || (i == 0 ? z.prefix_len : len - z.prefix_len) <= 0) continue;
+      const Pieces& part = p.part[i];
+      const int in_item = i == 0 ? b * z.GL + rr : rr;
+      const int id = (i == 0 ? kv : kv * z.B + b) * part.groups + in_item / part.group;
+      join_pieces<D>(s, part, part.info[id], id, in_item % part.group, c4, f, F);
     }
   }
-  if (W > 1) {
-#pragma unroll
-    for (int e = 0; e < kE; ++e) s_o[warp][e * 32 + lane] = o[e];
-    if (lane == 0) s_ml[warp] = make_float2(s.m, s.l);
+  if (F > 1) {
+    const int at = chunk * 32 + lane;
+    if (f > 0) {
+      s_o[f - 1][at] = s.o;
+      s_ml[f - 1][at] = make_float2(s.m, s.l);
+    }
     __syncthreads();
-    if (warp > 0) return;
+    if (f > 0) return;
 #pragma unroll
-    for (int w = 1; w < W; ++w) join_one<D>(o, s, s_o[w], s_ml[w]);
+    for (int i = 0; i < F - 1; ++i) join_one(s, s_ml[i][at], s_o[i][at]);
   }
-  store_row<D>(p, row, o, s);
+  if (live) store_row<D>(p, row, c4, s);
 }
 
 // Joint items: block (x, y) joins eight rows of the item that is cut where CTA
 // x's piece begins, if that is its first cut; x = 0: rows of sequences without keys.
 template <int D>
-__global__ void __launch_bounds__(256) join_cuts_kernel(const __grid_constant__ Params p) {
-  constexpr int kE = D / 32;
+__global__ void __launch_bounds__(D * 2) join_cuts_kernel(const __grid_constant__ Params p) {
   const Sizes& z = p.z;
-  const int warp = threadIdx.x >> 5;
-  float o[kE];
-#pragma unroll
-  for (int e = 0; e < kE; ++e) o[e] = 0.0f;
-  Joined s{-INFINITY, 0.0f};
-  if (!prefix_ok(p.c, p.lens, p.prefix_seq, z.prefix_len)) return;
+  const int lane = lane_id();
+  const int c4 = (threadIdx.x >> 5) * 4 + (lane & 3);
+  Joined s{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
   if (blockIdx.x == 0) {
     if (z.prefix_len > 0) return;
     const int64_t per = static_cast<int64_t>(z.H_kv) * z.GL;
     for (int b = 0; b < z.B; ++b) {
       if (entry_len(p.c, p.lens, p.seqs[b]) != 0) continue;
-      for (int64_t i = blockIdx.y * 8 + warp; i < per; i += gridDim.y * 8)
-        store_row<D>(p, b * per + i, o, s);
+      for (int64_t i = blockIdx.y * 8 + (lane >> 2); i < per; i += gridDim.y * 8)
+        store_row<D>(p, b * per + i, c4, s);
     }
     return;
   }
-  const int cta = blockIdx.x;
-  const int id = p.head_item[cta];
+  const int id = p.head_item[blockIdx.x];
   if (id < 0) return;
   const Pieces& part = p.part[1];
   const int2 info = part.info[id];
-  if (info.x != cta - 1) return;  // an earlier cut's block has it
+  if (info.x != static_cast<int>(blockIdx.x) - 1) return;  // an earlier cut's block has it
   Item it;
   it.shared = 0;
   it.g = id % z.groups_s;
   it.b = id / z.groups_s % z.B;
   it.kv = id / z.groups_s / z.B;
-  const int r = blockIdx.y * 8 + warp;
+  const int r = blockIdx.y * 8 + (lane >> 2);
   if (r >= rows_of(z.GL, it.g, z.group)) return;
-  int64_t at = static_cast<int64_t>(info.x) * kGroup + r;
-  join_one<D>(o, s, part.first_o + at * D, part.first_ml[at]);
-  for (int i = 1; i < info.y; ++i) {
-    at += kGroup;
-    join_one<D>(o, s, part.head_o + at * D, part.head_ml[at]);
-  }
-  store_row<D>(p, q_row(z, it, r), o, s);
+  join_pieces<D>(s, part, info, info.x, r, c4, 0, 1);
+  store_row<D>(p, q_row(z, it, r), c4, s);
 }
 
 inline int groups(int rows, int group) { return (rows + group - 1) / group; }
@@ -1245,6 +1278,7 @@ inline Form form_of(int B, int GL, bool prefix) {
 
 struct Place {
   size_t info, first_o, first_ml, head_o, head_ml;
+  int stride, group, groups;
 };
 struct Layout {
   Place part[2];
@@ -1252,7 +1286,6 @@ struct Layout {
 };
 Layout layout(const CacheDims& c, int32_t B, int32_t H, int32_t Lq, Form form) {
   const int GL = H / c.H_kv * Lq;
-  const size_t rows = static_cast<size_t>(B) * H * Lq;
   Layout l;
   memset(&l, 0, sizeof(l));
   size_t at = 0;
@@ -1264,17 +1297,21 @@ Layout layout(const CacheDims& c, int32_t B, int32_t H, int32_t Lq, Form form) {
   l.head_item = take(kMaxCtas * sizeof(int32_t));
   for (int i = 0; i < 2; ++i) {
     if (form == kJoint && i == 0) continue;
+    Place& t = l.part[i];
     const bool few = form == kFew || (form == kMixed && i == 1);
-    const int group = few ? kFewRows : kGroup;
-    const size_t slots = few ? kFewCtas * kFewRows : kMaxCtas * kGroup;
-    const size_t items = i == 0 ? static_cast<size_t>(c.H_kv) * groups(B * GL, group)
-                                : static_cast<size_t>(c.H_kv) * B * groups(GL, group);
-    const size_t firsts = form == kJoint ? slots : rows;
-    l.part[i].info = take(items * sizeof(int2));
-    l.part[i].first_o = take(firsts * c.d * sizeof(float));
-    l.part[i].first_ml = take(firsts * sizeof(float2));
-    l.part[i].head_o = take(slots * c.d * sizeof(float));
-    l.part[i].head_ml = take(slots * sizeof(float2));
+    const int all = i == 0 ? B * GL : GL;
+    t.group = few ? kFewRows : kGroup;
+    t.groups = groups(all, t.group);
+    // tile slots hold whole warps of rows, so that a warp's stores are whole lines
+    t.stride = few ? all : all < kGroup ? (all + 31) / 32 * 32 : kGroup;
+    const size_t items = static_cast<size_t>(c.H_kv) * (i == 0 ? 1 : B) * t.groups;
+    const size_t heads = static_cast<size_t>(few ? kFewCtas : kMaxCtas) * t.stride;
+    const size_t firsts = form == kJoint ? heads : items * t.stride;
+    t.info = take(items * sizeof(int2));
+    t.first_o = take(firsts * c.d * sizeof(float));
+    t.first_ml = take(firsts * sizeof(float2));
+    t.head_o = take(heads * c.d * sizeof(float));
+    t.head_ml = take(heads * sizeof(float2));
   }
   l.bytes = at;
   return l;
@@ -1340,10 +1377,17 @@ cudaError_t launch(const PrefixArgs& a, Params& p, Form form, int sms, cudaStrea
     if ((e = launch_tiles<D>(p, stream)) != cudaSuccess) return e;
   }
   if (form == kJoint) {
-    join_cuts_kernel<D><<<dim3(p.z.n_ctas, kGroup / 8), 256, 0, stream>>>(p);
+    join_cuts_kernel<D><<<dim3(p.z.n_ctas, kGroup / 8), D * 2, 0, stream>>>(p);
   } else {
+    // One row's pieces in turn, or by four warps where there are few rows and so
+    // many pieces of each.
     const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.Lq;
-    join_rows_kernel<D, 4><<<static_cast<unsigned>(rows), 128, 0, stream>>>(p);
+    const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+    if (grid >= 148) {
+      join_rows_kernel<D, 1><<<grid, D * 2, 0, stream>>>(p);
+    } else {
+      join_rows_kernel<D, 4><<<grid, D * 8, 0, stream>>>(p);
+    }
   }
   return cudaGetLastError();
 }
@@ -1366,7 +1410,8 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int* status, cudaStream
     const int32_t pool_rows = a.c.n_pages * a.c.H_kv * a.c.ps;
     const int box = a.c.ps < kBK ? a.c.ps : kBK;
     if (!make_tmap_bf16(&p.tm_k, a.k_pages, a.c.d, pool_rows, 1, box) ||
-        !make_tmap_bf16(&p.tm_v, a.v_pages, a.c.d, pool_rows, 1, box))
+        !make_tmap_bf16(&p.tm_v, a.v_pages, a.c.d, pool_rows, 1, box) ||
+        !make_tmap_bf16(&p.tm_q, a.q, a.c.d, a.B * a.H * a.Lq, 1, 128))
       return cudaErrorInvalidValue;
   }
   int dev = 0, sms = 0;
@@ -1391,14 +1436,18 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int* status, cudaStream
   p.head_item = reinterpret_cast<int32_t*>(ws + l.head_item);
   for (int i = 0; i < 2; ++i) {
     const bool few = form == kFew || (form == kMixed && i == 1);
+    const Place& at = l.part[i];
     Pieces& t = p.part[i];
-    t.info = reinterpret_cast<int2*>(ws + l.part[i].info);
-    t.first_o = reinterpret_cast<float*>(ws + l.part[i].first_o);
-    t.first_ml = reinterpret_cast<float2*>(ws + l.part[i].first_ml);
-    t.head_o = reinterpret_cast<float*>(ws + l.part[i].head_o);
-    t.head_ml = reinterpret_cast<float2*>(ws + l.part[i].head_ml);
-    t.stride = few ? kFewRows : kGroup;
-    t.groups = groups(i == 0 ? a.B * GL : GL, t.stride);
+    t.info = reinterpret_cast<int2*>(ws + at.info);
+    t.first_o = reinterpret_cast<float4*>(ws + at.first_o);
+    t.first_ml = reinterpret_cast<float2*>(ws + at.first_ml);
+    t.head_o = reinterpret_cast<float4*>(ws + at.head_o);
+    t.head_ml = reinterpret_cast<float2*>(ws + at.head_ml);
+    t.stride = at.stride;
+    t.group = at.group;
+    t.groups = at.groups;
+    t.rs = few ? a.c.d / 4 : 1;
+    t.cs = few ? 1 : at.stride;
   }
   return a.c.d == 128 ? launch<128>(a, p, form, sms, stream) : launch<64>(a, p, form, sms, stream);
 }
