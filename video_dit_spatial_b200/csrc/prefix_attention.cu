@@ -29,7 +29,7 @@
 //   one tile   up to 128 rows: tile A and tile B hold the SAME rows, A takes
 //              the even blocks and B the odd ones, so that one's softmax
 //              overlaps the other's products, and the two are joined in the epilogue.
-// Tensor memory: S_A 0, O_A 128, S_B 256, O_B 384; P (bf16) overwrites S. The
+// Tensor memory holds S and O of both tiles; P (bf16) overwrites S at d = 128. The
 // weights are rounded to bf16 because the tensor core multiplies them with bf16 values
 // (off by at most 2^-8 of each); row sums are taken before that rounding, in
 // fp32, as are the maxima and O.
@@ -111,10 +111,26 @@ struct __align__(64) Params {
   Pieces part[2];      // shared, own
 };
 
+// What the roles of a CTA need to know of a piece of an item, in shared memory: the
+// query-row warp walks the line of cost, the others read.
+struct __align__(16) Order {
+  int shared, kv, rows;
+  int lo, hi, nb;         // blocks [lo, hi) of nb; hi = 0: no more items
+  int pre, hi_pre;        // the first `pre` blocks are the prefix's, the last of which has hi_pre keys
+  int lo_own, hi_last;    // keys that count of the first block after them begin at lo_own, of the
+                          // last one end at hi_last
+  int seq, blk0;          // its sequence, and the number there of the first block after the prefix
+  int row0;               // first q row (items of one sequence)
+  int id, pieces;         // number, and pieces it is cut into
+  int unused;
+};
+constexpr int kOrders = 4;
+
 struct Barriers {
+  uint64_t item_full[kOrders], item_empty[kOrders];
   uint64_t q_full[2], q_empty[2];
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_full[2], o_final[2];
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_final[2];
   uint64_t o_free, ml_full, drain;
   uint32_t tmem_base;
   int abort_flag;
@@ -126,12 +142,21 @@ struct Cfg {
   static constexpr int kPanel = 128 * 128;              // 128 rows x 128 B
   static constexpr int kTile = kPanels * kPanel;        // one Q, K or V tile
   static constexpr int kStages = D == 128 ? 2 : 4;
+  // Tensor memory. At d = 64 there is room for P beside S: the next S = Q K^T of a
+  // tile then starts as soon as its S is in registers, and not after P V.
+  static constexpr bool kOwnP = D == 64;
+  static __device__ __forceinline__ uint32_t col_s(int t) { return t * (kOwnP ? 128 : 256); }
+  static __device__ __forceinline__ uint32_t col_p(int t) { return kOwnP ? 256 + t * 64 : col_s(t); }
+  static __device__ __forceinline__ uint32_t col_o(int t) {
+    return kOwnP ? 384 + t * 64 : 128 + t * 256;
+  }
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + 2 * kTile;
   static constexpr int kOffV = kOffK + kStages * kTile;
   static constexpr int kOffMl = kOffV + kStages * kTile;          // float2 [2][2][128]
   static constexpr int kOffBar = kOffMl + 2 * 2 * 128 * 8;
-  static constexpr int kOffBatch = kOffBar + 512;                 // cum, seq, len
+  static constexpr int kOffOrder = kOffBar + 512;
+  static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);  // cum, seq, len
   static constexpr int kUsed = kOffBatch + (kMaxBatch + 1) * 8 + 2 * kMaxBatch * 4 + 1024;
   static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA per SM
   static_assert(sizeof(Barriers) <= 512, "barriers");
@@ -352,6 +377,12 @@ __device__ __forceinline__ int64_t slot_of(const Params& p, const Item& it) {
   return it.lo > 0 || p.z.joint ? blockIdx.x : it.id;
 }
 
+// One arrival for a warp's 32: arrivals on one address are taken one by one.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if (lane_id() == 0) mbar_arrive(bar);
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -368,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* sV = smem + C::kOffV;
   float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   Barriers* bar = reinterpret_cast<Barriers*>(smem + C::kOffBar);
+  Order* s_order = reinterpret_cast<Order*>(smem + C::kOffOrder);
   int64_t* s_cum = reinterpret_cast<int64_t*>(smem + C::kOffBatch);
   int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 1);
   int* s_len = s_seq + kMaxBatch;
@@ -399,7 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar->q_full[s], 32);
       mbar_init(&bar->q_empty[s], 1);
       mbar_init(&bar->s_full[s], 1);
-      mbar_init(&bar->p_full[s], 128);
+      mbar_init(&bar->s_free[s], 4);  // warps
+      mbar_init(&bar->p_full[s], 4);
+      mbar_init(&bar->pv_done[s], 1);
       mbar_init(&bar->o_final[s], 1);
     }
     for (int s = 0; s < C::kStages; ++s) {
@@ -408,8 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar->v_full[s], 1);
       mbar_init(&bar->v_empty[s], 1);
     }
-    mbar_init(&bar->o_free, 256);
-    mbar_init(&bar->ml_full, 256);
+    for (int s = 0; s < kOrders; ++s) {
+      mbar_init(&bar->item_full[s], 1);
+      mbar_init(&bar->item_empty[s], 11);  // K, V and MMA warps, eight softmax warps
+    }
+    mbar_init(&bar->o_free, 8);
+    mbar_init(&bar->ml_full, 8);
     mbar_init(&bar->drain, 1);
     bar->abort_flag = 0;
     fence_mbar_init();
@@ -418,8 +456,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
 
-  Walk walk(z, s_cum, from, to);
-  Item it;
+  // The next order for this warp; false: there is none (or a wait ran out). Every
+  // lane reads it; `done` hands its place back.
+  int taken = 0;
+  auto take = [&](Order& it) {
+    const bool ok =
+        mbar_wait(&bar->item_full[taken % kOrders], (taken / kOrders) & 1, abort_flag, p.status);
+    if (!ok) return false;
+    it = s_order[taken % kOrders];
+    return it.hi > 0;
+  };
+  auto done = [&]() { mbar_arrive(&bar->item_empty[taken++ % kOrders]); };
+  Order it = {};
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kKWarp || warp == kVWarp) {
@@ -438,27 +486,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int bx = lane % boxes, pn = lane / boxes;
       const bool loads = pn < C::kPanels;
       const int past = p.c.n_pages * p.c.H_kv * p.c.ps;
-      auto page_of = [&](const Block& blk) {  // -1: no row of this lane's box counts
-        if (!loads || bx * box >= blk.hi || (bx + 1) * box <= blk.lo) return -1;
-        const int page = __ldg(p.table + static_cast<int64_t>(blk.seq) * p.c.max_pages +
-                               (blk.blk * kBK + bx * box) / p.c.ps);
-        if (page >= 0 && page < p.c.n_pages) return page;
+      // row of the pool that this lane's box of block k begins at
+      auto row_of = [&](int k) {
+        const bool own = k >= it.pre;
+        const int lo = k == it.pre ? it.lo_own : 0;
+        const int hi = k == it.pre - 1 ? it.hi_pre : own && k == it.nb - 1 ? it.hi_last : kBK;
+        if (!loads || bx * box >= hi || (bx + 1) * box <= lo) return past;
+        const int pos = (own ? k - it.pre + it.blk0 : k) * kBK + bx * box;
+        const int page = __ldg(p.table + static_cast<int64_t>(own ? it.seq : p.prefix_seq) * p.c.max_pages +
+                               pos / p.c.ps);
+        if (page >= 0 && page < p.c.n_pages)
+          return (page * p.c.H_kv + it.kv) * p.c.ps + pos % p.c.ps;
         atomicOr(p.status, kDevErrBounds);
-        return -1;
+        return past;
       };
       int n = 0;  // blocks issued
       bool ok = true;
-      while (ok && walk.next(it)) {
-        Block blk = block_of<kBK>(z, p.prefix_seq, s_seq, s_len, it, it.lo);
-        int page = page_of(blk);
+      while (ok && take(it)) {
+        __syncwarp();
+        if (lane == 0) done();
+        else ++taken;
+        int y = row_of(it.lo);
         for (int k = it.lo; k < it.hi; ++k, ++n) {
-          const int y = page < 0 ? past
-                                 : (page * p.c.H_kv + it.kv) * p.c.ps +
-                                       (blk.blk * kBK + bx * box) % p.c.ps;
-          if (k + 1 < it.hi) {  // the next block's pages, while this one waits
-            blk = block_of<kBK>(z, p.prefix_seq, s_seq, s_len, it, k + 1);
-            page = page_of(blk);
-          }
+          const int y0 = y;
+          if (k + 1 < it.hi) y = row_of(k + 1);  // the next block's page, while this one waits
           const int st = n % C::kStages;
           if (lane == 0) {
             ok = mbar_wait(&empty[st], ((n / C::kStages) & 1) ^ 1, abort_flag, p.status);
@@ -468,10 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           if (loads)
             tma_load_3d(ring + st * C::kTile + pn * C::kPanel + bx * box * 128, map, &full[st],
-                        pn * 64, y, 0);
+                        pn * 64, y0, 0);
         }
       }
-      if (!ok && lane == 0) {
+      if (*abort_flag && lane == 0) {
         // Let every copy this warp started land before the CTA retires.
         for (int j = (n > C::kStages ? n - C::kStages : 0); j < n; ++j) {
           const long long t0 = clock64();
@@ -482,99 +533,108 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
-      if (lane_id() == 0) {
-        constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBK, false, false);
-        constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
-        const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), v_addr = smem_u32(sV);
-        int n0 = 0, qn = 0, items = 0;
-        uint32_t pp = 0;  // bit t: parity of the next P of softmax warpgroup t
-        bool ok = true;
-        auto qk = [&](int t, int slot, int st) {
-          const uint32_t a0 = q_addr + slot * C::kTile, b0 = k_addr + st * C::kTile;
+      // The whole warp runs this, so that what the products take (descriptors,
+      // addresses) is uniform; one lane issues them.
+      constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBK, false, false);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, false, true);
+      const bool on = elect_one();
+      const uint64_t q_desc = sdesc_sw128(smem_u32(sQ), 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(smem_u32(sK), 16, 1024);
+      const uint64_t v_desc = sdesc_sw128(smem_u32(sV), C::kPanel, 1024);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      int n0 = 0, qn = 0, items = 0;  // blocks, query tiles, items so far
+      uint32_t pp = 0;                // bit t: parity of the next P of softmax warpgroup t
+      uint32_t sf = 3;                // bit t: parity of tile t's last but one reading of S
+      bool ok = true;
+      auto qk = [&](int t, int slot, int st) {
+        const uint64_t a = q_desc + slot * (C::kTile >> 4), b = k_desc + st * (C::kTile >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * C::kPanel + (kk & 3) * 32;
-            mma_bf16_ss(tmem + t * 256, sdesc_sw128(a0 + off, 16, 1024),
-                        sdesc_sw128(b0 + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
-          }
-          tc_commit(&bar->s_full[t]);
-        };
-        auto pv = [&](int t, int st, bool first) {
-          const uint32_t b0 = v_addr + st * C::kTile;
+        for (int kk = 0; kk < D / 16; ++kk) {
+          constexpr int kUnit = 16;
+          const int off = ((kk >> 2) * C::kPanel + (kk & 3) * 32) / kUnit;
+          mma_bf16_ss_on(on, tm + C::col_s(t), a + off, b + off, idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        tc_commit_on(on, &bar->s_full[t]);
+      };
+      auto pv = [&](int t, int st, bool first) {
+        const uint64_t b = v_desc + st * (C::kTile >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk)
-            mma_bf16_ts(tmem + t * 256 + 128, tmem + t * 256 + kk * 8,
-                        sdesc_sw128(b0 + kk * 16 * 128, C::kPanel, 1024), idesc_pv,
-                        (!first || kk > 0) ? 1u : 0u);
-        };
-        auto wait_p = [&](int t) {
-          ok = ok && mbar_wait(&bar->p_full[t], (pp >> t) & 1u, abort_flag, p.status);
-          pp ^= 1u << t;
-          return ok;
-        };
-        auto wait = [&](uint64_t* b, uint32_t parity) {
-          if (ok) ok = mbar_wait(b, parity, abort_flag, p.status);
-          return ok;
-        };
-        while (ok && walk.next(it)) {
-          const int n = it.hi - it.lo;
-          const bool two = it.rows > 128;
-          for (int j = 0; ok && j <= n; ++j) {
-            const int st = (n0 + j) % C::kStages, par = ((n0 + j) / C::kStages) & 1;
-            const int pst = (n0 + j - 1 + C::kStages) % C::kStages;
-            const int ppar = ((n0 + j - 1) / C::kStages) & 1;
-            if (j == 1 && items > 0 && !wait(&bar->o_free, (items - 1) & 1)) break;
-            if (two) {
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          mma_bf16_ts_on(on, tm + C::col_o(t), tm + C::col_p(t) + kk * 8, b + kk * 128, idesc_pv,
+                         (!first || kk > 0) ? 1u : 0u);
+        if (C::kOwnP) tc_commit_on(on, &bar->pv_done[t]);
+      };
+      auto ready = [&](uint64_t* b, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_test(b, parity)) != 0;
+      };
+      while (take(it)) {
+        __syncwarp();
+        if (on) {
+          done();
+        } else {
+          ++taken;
+        }
+        const int n = __shfl_sync(0xffffffffu, it.hi - it.lo, 0);
+        const bool two = __shfl_sync(0xffffffffu, it.rows, 0) > 128;
+        // The products that may come next (two tiles, Q K^T or P V) are issued as
+        // their operands get ready; in a fixed order one tile waits for what
+        // the other's softmax has still to do. With one tile of rows tile 1 has the odd
+        // blocks. S of a tile is overwritten once it was read (P apart) or after its
+        // P V (products complete in the order of issue).
+        const int step = two ? 1 : 2;
+        int q[2] = {0, two ? 0 : 1}, v[2] = {0, two ? 0 : 1};  // next block of each
+        long long idle = 0;                                    // since when nothing was ready
+        while (v[0] < n || v[1] < n) {
+          bool did = false;
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                if (j > 0) {
-                  if (t == 0 && !wait(&bar->v_full[pst], ppar)) break;
-                  if (!wait_p(t)) break;
-                  tc_fence_after();
-                  pv(t, pst, j == 1);
-                  if (t == 1) tc_commit(&bar->v_empty[pst]);
-                  if (j == n) tc_commit(&bar->o_final[t]);
-                }
-                if (j < n) {
-                  if (j == 0 && !wait(&bar->q_full[(qn + t) & 1], ((qn + t) >> 1) & 1)) break;
-                  if (t == 0 && !wait(&bar->k_full[st], par)) break;
-                  tc_fence_after();
-                  qk(t, (qn + t) & 1, st);
-                  if (j == n - 1) tc_commit(&bar->q_empty[(qn + t) & 1]);
-                }
-              }
-              if (!ok) break;
-              if (j < n) tc_commit(&bar->k_empty[st]);
-            } else {
-              if (j < n) {
-                if (j == 0 && !wait(&bar->q_full[qn & 1], (qn >> 1) & 1)) break;
-                if (!wait(&bar->k_full[st], par)) break;
-                tc_fence_after();
-                qk(j & 1, qn & 1, st);
-                tc_commit(&bar->k_empty[st]);
-                if (j == n - 1) tc_commit(&bar->q_empty[qn & 1]);
-              }
-              if (j > 0) {
-                const int t = (j - 1) & 1;
-                if (!wait(&bar->v_full[pst], ppar)) break;
-                if (!wait_p(t)) break;
-                tc_fence_after();
-                pv(t, pst, j <= 2);
-                tc_commit(&bar->v_empty[pst]);
-                if (j >= n - 1) tc_commit(&bar->o_final[t]);  // the tile's last block
-              }
+          for (int t = 0; t < 2; ++t) {
+            const int vst = (n0 + v[t]) % C::kStages, kst = (n0 + q[t]) % C::kStages;
+            if (v[t] < q[t] && v[t] < n && ready(&bar->p_full[t], (pp >> t) & 1u) &&
+                ready(&bar->v_full[vst], ((n0 + v[t]) / C::kStages) & 1) &&
+                (v[t] >= step || items == 0 || ready(&bar->o_free, (items - 1) & 1))) {
+              tc_fence_after();
+              pv(t, vst, v[t] < step);
+              pp ^= 1u << t;
+              v[t] += step;
+              if (!two || v[1 - t] >= v[t]) tc_commit_on(on, &bar->v_empty[vst]);
+              if (v[t] >= n) tc_commit_on(on, &bar->o_final[t]);
+              did = true;
+            }
+            const int slot = (qn + (two ? t : 0)) & 1;
+            if (q[t] < n && (C::kOwnP ? ready(&bar->s_free[t], (sf >> t) & 1u) : v[t] == q[t]) &&
+                ready(&bar->k_full[kst], ((n0 + q[t]) / C::kStages) & 1) &&
+                (q[t] >= step || ready(&bar->q_full[slot], ((qn + (two ? t : 0)) >> 1) & 1))) {
+              tc_fence_after();
+              qk(t, slot, kst);
+              sf ^= 1u << t;
+              q[t] += step;
+              if (!two || q[1 - t] >= q[t]) tc_commit_on(on, &bar->k_empty[kst]);
+              if (q[t] >= n && (two || q[1 - t] >= n)) tc_commit_on(on, &bar->q_empty[slot]);
+              did = true;
             }
           }
-          n0 += n;
-          qn += two ? 2 : 1;
-          ++items;
-        }
-        if (!ok) {
-          // Retire every MMA issued so far before tensor memory is released.
-          tc_commit(&bar->drain);
-          const long long t0 = clock64();
-          while (!mbar_try_wait(&bar->drain, 0) && clock64() - t0 < kWaitLimitCycles) {
+          if (did) {
+            idle = 0;
+          } else if (idle == 0) {
+            idle = clock64();
+          } else if (__any_sync(0xffffffffu,
+                                *abort_flag || clock64() - idle > kWaitLimitCycles)) {
+            if (!*abort_flag && on) atomicOr(p.status, kDevErrTimeout);
+            *abort_flag = 1;
+            ok = false;
+            break;
           }
+        }
+        if (!ok) break;
+        n0 += n;
+        qn += two ? 2 : 1;
+        ++items;
+      }
+      if (*abort_flag) {
+        // Retire every MMA issued so far before tensor memory is released.
+        tc_commit_on(on, &bar->drain);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&bar->drain, 0) && clock64() - t0 < kWaitLimitCycles) {
         }
       }
     } else {
@@ -588,17 +648,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vec = lane % kVecs;
       int qn = 0;
       bool ok = true;
-      while (ok && walk.next(it)) {
-        for (int r0 = 0; r0 < it.rows; r0 += 128, ++qn) {
+      Walk walk(z, s_cum, from, to);
+      Item item;
+      for (bool more = true; more; ++taken) {
+        more = walk.next(item);
+        Order* order = &s_order[taken % kOrders];
+        ok = mbar_wait(&bar->item_empty[taken % kOrders], ((taken / kOrders) & 1) ^ 1, abort_flag,
+                       p.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          Order w;
+          memset(&w, 0, sizeof(w));
+          if (more) {
+            w.shared = item.shared;
+            w.kv = item.kv;
+            w.rows = item.rows;
+            w.lo = item.lo;
+            w.hi = item.hi;
+            w.nb = item.nb;
+            w.pre = item.shared || z.joint ? z.nbp : 0;
+            w.hi_pre = z.prefix_len - (z.nbp - 1) * kBK;
+            w.lo_own = z.prefix_len % kBK;
+            w.blk0 = z.prefix_len / kBK;
+            if (!item.shared) {
+              w.seq = s_seq[item.b];
+              w.hi_last = s_len[item.b] - (w.blk0 + item.nb - w.pre - 1) * kBK;
+              w.row0 = static_cast<int>(q_row(z, item, 0));
+            }
+            w.id = item.id;
+            if (item.lo == 0) w.pieces = pieces_of(item, walk.at, total, n_pieces).y;
+          }
+          *order = w;
+          mbar_arrive(&bar->item_full[taken % kOrders]);
+        }
+        if (!more) break;
+        for (int r0 = 0; r0 < item.rows; r0 += 128, ++qn) {
           uint64_t* full = &bar->q_full[qn & 1];
           ok = mbar_wait(&bar->q_empty[qn & 1], ((qn >> 1) & 1) ^ 1, abort_flag, p.status);
           if (!__all_sync(0xffffffffu, ok)) {
-            ok = false;
+            ok = more = false;
             break;
           }
-          if (!it.shared) {
+          if (!item.shared) {
             if (lane == 0) {
-              const int64_t row = q_row(z, it, r0);
+              const int64_t row = q_row(z, item, r0);
               mbar_arrive_expect_tx(full, C::kTile);
               for (int pn = 0; pn < C::kPanels; ++pn)
                 tma_load_3d(sQ + (qn & 1) * C::kTile + pn * C::kPanel, &p.tm_q, full, pn * 64,
@@ -608,18 +704,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             continue;
           }
+          // lane i finds the rows i, i + 32, ... and hands them round
           const uint32_t dst = q_addr + (qn & 1) * C::kTile + (vec >> 3) * C::kPanel;
-          const int rows = min(it.rows - r0, 128);
+          const int rows = min(item.rows - r0, 128);
+          for (int r1 = 0; r1 < rows; r1 += 32) {
+            const int mine = r1 + lane < rows ? static_cast<int>(q_row(z, item, r0 + r1 + lane)) : 0;
 #pragma unroll 8
-          for (int r = lane / kVecs; r < rows; r += 32 / kVecs)
-            cp_async16(dst + r * 128 + (((vec & 7) ^ (r & 7)) << 4),
-                       p.q + q_row(z, it, r0 + r) * D + vec * 8);
+            for (int i = lane / kVecs; i < 32; i += 32 / kVecs) {
+              const int src = __shfl_sync(0xffffffffu, mine, i);
+              const int r = r1 + i;
+              if (r < rows)
+                cp_async16(dst + r * 128 + (((vec & 7) ^ (r & 7)) << 4),
+                           p.q + static_cast<int64_t>(src) * D + vec * 8);
+            }
+          }
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();
           mbar_arrive(full);
         }
       }
-      if (!ok && lane == 0) {
+      if (*abort_flag && lane == 0) {
         // Let the tiled loads this warp started land before the CTA retires.
         for (int j = (qn > 2 ? qn - 2 : 0); j < qn; ++j) {
           const long long t0 = clock64();
@@ -635,34 +739,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2;
     const int r = tid & 127;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t s_col = lanes + t * 256, o_col = s_col + 128;
+    const uint32_t s_col = lanes + C::col_s(t), p_col = lanes + C::col_p(t);
+    const uint32_t o_col = lanes + C::col_o(t);
     int n0 = 0, sc = 0, ones = 0;
     uint32_t fp = 0;  // bit t: parity of the next final commit of tile t
     bool ok = true;
     if (z.joint && tid == 0) p.head_item[cta] = -1;
-    while (ok && walk.next(it)) {
+    while (ok && take(it)) {
+      __syncwarp();
+      if (lane_id() == 0) done();
+      else ++taken;
       const int n = it.hi - it.lo;
       const bool two = it.rows > 128;
       const int rows = two ? min(max(it.rows - t * 128, 0), 128) : it.rows;
       const bool active = (warp & 3) * 32 < rows;  // warp-uniform
       float m = -INFINITY, l = 0.0f;                // log2 units
       for (int j = two ? 0 : t; j < n; j += two ? 1 : 2, ++sc) {
-        const Block blk = block_of<kBK>(z, p.prefix_seq, s_seq, s_len, it, it.lo + j);
-        const bool ragged = blk.lo > 0 || blk.hi < kBK;
+        const int k = it.lo + j;
+        const int k_lo = k == it.pre ? it.lo_own : 0;  // the keys of this block that count
+        const int k_hi =
+            k == it.pre - 1 ? it.hi_pre : k >= it.pre && k == it.nb - 1 ? it.hi_last : kBK;
+        const bool ragged = k_lo > 0 || k_hi < kBK;
         ok = mbar_wait(&bar->s_full[t], sc & 1, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
+        uint32_t sr[kBK];
         if (active) {
-          uint32_t sr[kBK];
 #pragma unroll
           for (int ch = 0; ch < kBK / 32; ++ch)
             tmem_ld_32x32b_x32(s_col + ch * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[ch * 32]));
           tmem_ld_wait();
           reg_fence(sr);
+        }
+        if (C::kOwnP) {
+          tc_fence_before();
+          warp_arrive(&bar->s_free[t]);
+          // P and O are free again: the previous block's product is done
+          if (sc > 0) ok = mbar_wait(&bar->pv_done[t], (sc - 1) & 1, abort_flag, p.status);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (active) {
           if (ragged) {
 #pragma unroll
             for (int i = 0; i < kBK; ++i)
-              if (i < blk.lo || i >= blk.hi) sr[i] = __float_as_uint(-INFINITY);
+              if (i < k_lo || i >= k_hi) sr[i] = __float_as_uint(-INFINITY);
           }
           float xm[8];
 #pragma unroll
@@ -694,12 +815,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               fadd2(s0, s1, s0, s1, e0, e1);
               pk[i] = pack_bf16x2(e0, e1);
             }
-            tmem_st_32x32b_x16(s_col + ch * 16, pk);
+            tmem_st_32x32b_x16(p_col + ch * 16, pk);
           }
           l = l * alpha + (s0 + s1);
           m = m_new;
           tmem_st_wait();
-          // This tile's previous PV retired with the commit of this S.
+          // This tile's previous PV has retired: with the commit of this S, or waited for.
           if (j >= (two ? 1 : 2) && __any_sync(0xffffffffu, rebase)) {
 #pragma unroll
             for (int ch = 0; ch < D / 32; ++ch) {
@@ -715,13 +836,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // Values that do not count may hold anything; a weight of 0 times NaN is
-        // NaN, so their rows are cleared before the product reads them (with two
-        // tiles by the first one's threads: its product comes first).
-        if (ragged && (!two || t == 0)) {
+        // NaN, so their rows are cleared before the product reads them (by
+        // both tiles' threads: either product may come first).
+        if (ragged) {
           const int st = (n0 + j) % C::kStages;
           ok = mbar_wait(&bar->v_full[st], ((n0 + j) / C::kStages) & 1, abort_flag, p.status);
           if (!ok) break;
-          if (r < blk.lo || r >= blk.hi) {
+          if (r < k_lo || r >= k_hi) {
 #pragma unroll
             for (int pn = 0; pn < C::kPanels; ++pn) {
               uint4* row = reinterpret_cast<uint4*>(sV + st * C::kTile + pn * C::kPanel + r * 128);
@@ -732,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         }
         tc_fence_before();
-        mbar_arrive(&bar->p_full[t]);
+        warp_arrive(&bar->p_full[t]);
       }
       if (!ok) break;
 
@@ -744,7 +865,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!two) {
         float2* ml = s_ml + (ones & 1) * 256;
         ml[t * 128 + r] = make_float2(m, l);
-        mbar_arrive(&bar->ml_full);
+        warp_arrive(&bar->ml_full);
         ok = mbar_wait(&bar->ml_full, ones & 1, abort_flag, p.status);
         if (!ok) break;
         ++ones;
@@ -768,9 +889,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int rr = two ? t * 128 + r : r;  // row of the item
       const bool valid = r < rows;
-      const int64_t row = valid ? q_row(z, it, rr) : 0;
+      const int64_t row = it.row0 + rr;
       const Pieces& part = p.part[it.shared ? 0 : 1];
-      const int64_t slot = slot_of(p, it) * part.stride;
+      const int64_t slot =
+          static_cast<int64_t>(it.lo > 0 || z.joint ? cta : it.id) * part.stride;
       float4* out = (it.lo > 0 ? part.head_o : part.first_o) + slot * (D / 4) + rr;
       float2* out_ml = (it.lo > 0 ? part.head_ml : part.first_ml) + slot + rr;
       const float inv_l = l > 0.0f ? 1.0f / l : 0.0f;
@@ -784,14 +906,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld_wait();
             reg_fence(o);
           } else {
-            tmem_ld_32x32b_x32(lanes + 128 + c0, o);
+            tmem_ld_32x32b_x32(lanes + C::col_o(0) + c0, o);
             tmem_ld_wait();
             reg_fence(o);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(u2f(o[i]) * fa);
             if (both) {
               uint32_t ob[32];
-              tmem_ld_32x32b_x32(lanes + 384 + c0, ob);
+              tmem_ld_32x32b_x32(lanes + C::col_o(1) + c0, ob);
               tmem_ld_wait();
               reg_fence(ob);
 #pragma unroll
@@ -819,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&bar->o_free);
+      warp_arrive(&bar->o_free);
       if (valid && (two || t == 0)) {
         if (!final_rows) {
           *out_ml = make_float2(m, l);
@@ -831,7 +953,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it.lo > 0) {
           if (z.joint) p.head_item[cta] = it.id;
         } else if (!final_rows) {
-          part.info[it.id] = pieces_of(it, walk.at, total, n_pieces);
+          part.info[it.id] = make_int2(cta, it.pieces);
         }
       }
       n0 += n;
