@@ -46,8 +46,8 @@ constexpr int kKWarp = 8;
 constexpr int kMmaWarp = 9;
 constexpr int kVWarp = 10;
 constexpr int kLaunchRegs = 168;
-constexpr int kSoftmaxRegs = 224;
-constexpr int kOtherRegs = 56;
+constexpr int kSoftmaxRegs = 216;
+constexpr int kOtherRegs = 72;
 static_assert(2 * kSoftmaxRegs + kOtherRegs == 3 * kLaunchRegs, "register split");
 constexpr float kRebaseLog2 = 8.0f;  // O is re-based when a maximum grows by more than 2^8
 constexpr int kBK = 128;             // keys of a block
@@ -55,9 +55,7 @@ constexpr int kGroup = 256;          // rows of an item
 constexpr int kMaxCtas = 148;
 constexpr int kMaxBatch = 1024;
 constexpr int kFewRows = 16;    // rows of an item of the few-row kernel
-constexpr int kFewWarps = 4;
-constexpr int kFewPerSm = 3;    // its CTAs per SM
-constexpr int kFewCtas = kMaxCtas * kFewPerSm;
+constexpr int kFewWarps = 4;    // of them that compute
 // Cost of a block: a two-tile block keeps the tensor core and the exponentials
 // busy for about 3.7k cycles, a one-tile block takes about as long as its
 // 64 KB take from HBM on every SM at once, 2.8k.
@@ -125,6 +123,25 @@ struct __align__(16) Order {
   int unused;
 };
 constexpr int kOrders = 4;
+
+// A reader's place in the ring of orders.
+struct Orders {
+  Order* ring;
+  uint64_t *full, *empty;
+  volatile int* abort_flag;
+  int* status;
+  int n = 0;
+  // The next order; false: there is none (or a wait ran out). Every lane of the warp calls it.
+  __device__ __forceinline__ bool take(Order& it) {
+    if (!mbar_wait(&full[n % kOrders], (n / kOrders) & 1, abort_flag, status)) return false;
+    it = ring[n % kOrders];
+    __syncwarp();
+    if (it.hi == 0) return false;
+    if (lane_id() == 0) mbar_arrive(&empty[n % kOrders]);
+    ++n;
+    return true;
+  }
+};
 
 struct Barriers {
   uint64_t item_full[kOrders], item_empty[kOrders];
@@ -270,30 +287,6 @@ struct Walk {
   }
 };
 
-// Where block k (of BK keys) of an item lies: block number `blk` of sequence
-// `seq`, of whose keys [lo, hi) count.
-struct Block {
-  int seq, blk, lo, hi;
-};
-template <int BK>
-__device__ __forceinline__ Block block_of(const Sizes& z, int prefix_seq, const int* s_seq,
-                                          const int* s_len, const Item& it, int k) {
-  Block r;
-  const int pre = it.shared || z.joint ? z.nbp : 0;
-  if (k < pre) {
-    r.seq = prefix_seq;
-    r.blk = k;
-    r.lo = 0;
-    r.hi = min(BK, z.prefix_len - k * BK);
-  } else {
-    r.seq = s_seq[it.b];
-    r.blk = k - pre + z.prefix_len / BK;
-    r.lo = max(0, z.prefix_len - r.blk * BK);
-    r.hi = min(BK, s_len[it.b] - r.blk * BK);
-  }
-  return r;
-}
-
 // q row (and o, lse row) of row r of an item.
 __device__ __forceinline__ int64_t q_row(const Sizes& z, const Item& it, int r) {
   r += it.g * z.group;
@@ -372,11 +365,6 @@ __device__ __forceinline__ int2 pieces_of(const Item& it, int64_t end, int64_t t
   return make_int2(blockIdx.x, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1);
 }
 
-// Slot of an item's piece in this CTA's hands.
-__device__ __forceinline__ int64_t slot_of(const Params& p, const Item& it) {
-  return it.lo > 0 || p.z.joint ? blockIdx.x : it.id;
-}
-
 // One arrival for a warp's 32: arrivals on one address are taken one by one.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
   __syncwarp();
@@ -385,6 +373,105 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The role of a warp that loads K or V: the blocks of every order, through a ring of
+// STAGES tiles of BK rows x D / 64 panels. A block is BK / box boxes of
+// min(page_size, BK) rows, times the panels; a lane loads one of them. Boxes without
+// a row that counts and pages past the pool are read from past the end of
+// the map: zeros.
+template <int D, int BK, int STAGES>
+__device__ __forceinline__ void stream_blocks(const Params& p, const CUtensorMap* map, uint8_t* ring,
+                                              uint64_t* full, uint64_t* empty, Orders& orders) {
+  constexpr int kPanels = D / 64, kPanel = BK * 128, kTile = kPanels * kPanel;
+  const int lane = lane_id();
+  const int box = min(p.c.ps, BK);
+  const int boxes = BK / box;
+  const int bx = lane % boxes, pn = lane / boxes;
+  const bool loads = pn < kPanels;
+  const int past = p.c.n_pages * p.c.H_kv * p.c.ps;
+  Order it = {};
+  // row of the pool that this lane's box of block k begins at
+  auto row_of = [&](int k) {
+    const bool own = k >= it.pre;
+    const int lo = k == it.pre ? it.lo_own : 0;
+    const int hi = k == it.pre - 1 ? it.hi_pre : own && k == it.nb - 1 ? it.hi_last : BK;
+    if (!loads || bx * box >= hi || (bx + 1) * box <= lo) return past;
+    const int pos = (own ? k - it.pre + it.blk0 : k) * BK + bx * box;
+    const int page = __ldg(p.table + static_cast<int64_t>(own ? it.seq : p.prefix_seq) * p.c.max_pages +
+                           pos / p.c.ps);
+    if (page >= 0 && page < p.c.n_pages)
+      return (page * p.c.H_kv + it.kv) * p.c.ps + pos % p.c.ps;
+    atomicOr(p.status, kDevErrBounds);
+    return past;
+  };
+  int n = 0;  // blocks issued
+  bool ok = true;
+  while (ok && orders.take(it)) {
+    int y = row_of(it.lo);
+    for (int k = it.lo; k < it.hi; ++k, ++n) {
+      const int y0 = y;
+      if (k + 1 < it.hi) y = row_of(k + 1);  // the next block's page, while this one waits
+      const int st = n % STAGES;
+      if (lane == 0) {
+        ok = mbar_wait(&empty[st], ((n / STAGES) & 1) ^ 1, orders.abort_flag, p.status);
+        if (ok) mbar_arrive_expect_tx(&full[st], kTile);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      if (loads)
+        tma_load_3d(ring + st * kTile + pn * kPanel + bx * box * 128, map, &full[st], pn * 64, y0, 0);
+    }
+  }
+  if (*orders.abort_flag && lane == 0) {
+    // Let every copy this warp started land before the CTA retires.
+    for (int j = (n > STAGES ? n - STAGES : 0); j < n; ++j) {
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&full[j % STAGES], (j / STAGES) & 1) &&
+             clock64() - t0 < kWaitLimitCycles) {
+      }
+    }
+  }
+}
+
+// The next item of the walk as an order (none: the end), for the warp that publishes
+// them. False: a wait ran out.
+template <int BK>
+__device__ __forceinline__ bool publish(const Params& p, Orders& orders, bool more, const Item& item,
+                                        const Walk& walk, int64_t total, int n_pieces,
+                                        const int* s_seq, const int* s_len) {
+  const Sizes& z = p.z;
+  const int at = orders.n % kOrders;
+  const bool ok = mbar_wait(&orders.empty[at], ((orders.n / kOrders) & 1) ^ 1, orders.abort_flag,
+                            p.status);
+  if (!__all_sync(0xffffffffu, ok)) return false;
+  if (lane_id() == 0) {
+    Order w;
+    memset(&w, 0, sizeof(w));
+    if (more) {
+      w.shared = item.shared;
+      w.kv = item.kv;
+      w.rows = item.rows;
+      w.lo = item.lo;
+      w.hi = item.hi;
+      w.nb = item.nb;
+      w.pre = item.shared || z.joint ? z.nbp : 0;
+      w.hi_pre = z.prefix_len - (z.nbp - 1) * BK;
+      w.lo_own = z.prefix_len % BK;
+      w.blk0 = z.prefix_len / BK;
+      if (!item.shared) {
+        w.seq = s_seq[item.b];
+        w.hi_last = s_len[item.b] - (w.blk0 + item.nb - w.pre - 1) * BK;
+        w.row0 = static_cast<int>(q_row(z, item, 0));
+      }
+      w.id = item.id;
+      if (item.lo == 0) w.pieces = pieces_of(item, walk.at, total, n_pieces).y;
+    }
+    orders.ring[at] = w;
+    mbar_arrive(&orders.full[at]);
+  }
+  ++orders.n;
+  return true;
 }
 
 template <int D>
@@ -456,81 +543,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bar->tmem_base;
 
-  // The next order for this warp; false: there is none (or a wait ran out). Every
-  // lane reads it; `done` hands its place back.
-  int taken = 0;
-  auto take = [&](Order& it) {
-    const bool ok =
-        mbar_wait(&bar->item_full[taken % kOrders], (taken / kOrders) & 1, abort_flag, p.status);
-    if (!ok) return false;
-    it = s_order[taken % kOrders];
-    return it.hi > 0;
-  };
-  auto done = [&]() { mbar_arrive(&bar->item_empty[taken++ % kOrders]); };
+  Orders orders{s_order, bar->item_full, bar->item_empty, abort_flag, p.status};
   Order it = {};
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kKWarp || warp == kVWarp) {
-      // ---------------------------------------------------------- K or V
-      // A block is 128 / box boxes of min(page_size, 128) rows, times the panels;
-      // a lane loads one of them. Boxes without a row that counts and pages
-      // past the pool are read from past the end of the map: zeros.
       const bool is_k = warp == kKWarp;
-      uint64_t* full = is_k ? bar->k_full : bar->v_full;
-      uint64_t* empty = is_k ? bar->k_empty : bar->v_empty;
-      const CUtensorMap* map = is_k ? &p.tm_k : &p.tm_v;
-      uint8_t* ring = is_k ? sK : sV;
-      const int lane = lane_id();
-      const int box = min(p.c.ps, kBK);
-      const int boxes = kBK / box;
-      const int bx = lane % boxes, pn = lane / boxes;
-      const bool loads = pn < C::kPanels;
-      const int past = p.c.n_pages * p.c.H_kv * p.c.ps;
-      // row of the pool that this lane's box of block k begins at
-      auto row_of = [&](int k) {
-        const bool own = k >= it.pre;
-        const int lo = k == it.pre ? it.lo_own : 0;
-        const int hi = k == it.pre - 1 ? it.hi_pre : own && k == it.nb - 1 ? it.hi_last : kBK;
-        if (!loads || bx * box >= hi || (bx + 1) * box <= lo) return past;
-        const int pos = (own ? k - it.pre + it.blk0 : k) * kBK + bx * box;
-        const int page = __ldg(p.table + static_cast<int64_t>(own ? it.seq : p.prefix_seq) * p.c.max_pages +
-                               pos / p.c.ps);
-        if (page >= 0 && page < p.c.n_pages)
-          return (page * p.c.H_kv + it.kv) * p.c.ps + pos % p.c.ps;
-        atomicOr(p.status, kDevErrBounds);
-        return past;
-      };
-      int n = 0;  // blocks issued
-      bool ok = true;
-      while (ok && take(it)) {
-        __syncwarp();
-        if (lane == 0) done();
-        else ++taken;
-        int y = row_of(it.lo);
-        for (int k = it.lo; k < it.hi; ++k, ++n) {
-          const int y0 = y;
-          if (k + 1 < it.hi) y = row_of(k + 1);  // the next block's page, while this one waits
-          const int st = n % C::kStages;
-          if (lane == 0) {
-            ok = mbar_wait(&empty[st], ((n / C::kStages) & 1) ^ 1, abort_flag, p.status);
-            if (ok) mbar_arrive_expect_tx(&full[st], C::kTile);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          if (loads)
-            tma_load_3d(ring + st * C::kTile + pn * C::kPanel + bx * box * 128, map, &full[st],
-                        pn * 64, y0, 0);
-        }
-      }
-      if (*abort_flag && lane == 0) {
-        // Let every copy this warp started land before the CTA retires.
-        for (int j = (n > C::kStages ? n - C::kStages : 0); j < n; ++j) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(&full[j % C::kStages], (j / C::kStages) & 1) &&
-                 clock64() - t0 < kWaitLimitCycles) {
-          }
-        }
-      }
+      stream_blocks<D, kBK, C::kStages>(p, is_k ? &p.tm_k : &p.tm_v, is_k ? sK : sV,
+                                        is_k ? bar->k_full : bar->v_full,
+                                        is_k ? bar->k_empty : bar->v_empty, orders);
     } else if (warp == kMmaWarp) {
       // ---------------------------------------------------------- MMA issuer
       // The whole warp runs this, so that what the products take (descriptors,
@@ -567,13 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto ready = [&](uint64_t* b, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_test(b, parity)) != 0;
       };
-      while (take(it)) {
-        __syncwarp();
-        if (on) {
-          done();
-        } else {
-          ++taken;
-        }
+      while (orders.take(it)) {
         const int n = __shfl_sync(0xffffffffu, it.hi - it.lo, 0);
         const bool two = __shfl_sync(0xffffffffu, it.rows, 0) > 128;
         // The products that may come next (two tiles, Q K^T or P V) are issued as
@@ -650,40 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Walk walk(z, s_cum, from, to);
       Item item;
-      for (bool more = true; more; ++taken) {
+      for (bool more = true; more;) {
         more = walk.next(item);
-        Order* order = &s_order[taken % kOrders];
-        ok = mbar_wait(&bar->item_empty[taken % kOrders], ((taken / kOrders) & 1) ^ 1, abort_flag,
-                       p.status);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          Order w;
-          memset(&w, 0, sizeof(w));
-          if (more) {
-            w.shared = item.shared;
-            w.kv = item.kv;
-            w.rows = item.rows;
-            w.lo = item.lo;
-            w.hi = item.hi;
-            w.nb = item.nb;
-            w.pre = item.shared || z.joint ? z.nbp : 0;
-            w.hi_pre = z.prefix_len - (z.nbp - 1) * kBK;
-            w.lo_own = z.prefix_len % kBK;
-            w.blk0 = z.prefix_len / kBK;
-            if (!item.shared) {
-              w.seq = s_seq[item.b];
-              w.hi_last = s_len[item.b] - (w.blk0 + item.nb - w.pre - 1) * kBK;
-              w.row0 = static_cast<int>(q_row(z, item, 0));
-            }
-            w.id = item.id;
-            if (item.lo == 0) w.pieces = pieces_of(item, walk.at, total, n_pieces).y;
-          }
-          *order = w;
-          mbar_arrive(&bar->item_full[taken % kOrders]);
-        }
+        if (!publish<kBK>(p, orders, more, item, walk, total, n_pieces, s_seq, s_len)) break;
         if (!more) break;
         for (int r0 = 0; r0 < item.rows; r0 += 128, ++qn) {
           uint64_t* full = &bar->q_full[qn & 1];
@@ -745,10 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t fp = 0;  // bit t: parity of the next final commit of tile t
     bool ok = true;
     if (z.joint && tid == 0) p.head_item[cta] = -1;
-    while (ok && take(it)) {
-      __syncwarp();
-      if (lane_id() == 0) done();
-      else ++taken;
+    while (ok && orders.take(it)) {
       const int n = it.hi - it.lo;
       const bool two = it.rows > 128;
       const int rows = two ? min(max(it.rows - t * 128, 0), 128) : it.rows;
@@ -774,10 +755,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (C::kOwnP) {
           tc_fence_before();
           warp_arrive(&bar->s_free[t]);
-          // P and O are free again: the previous block's product is done
-          if (sc > 0) ok = mbar_wait(&bar->pv_done[t], (sc - 1) & 1, abort_flag, p.status);
-          if (!ok) break;
-          tc_fence_after();
         }
         if (active) {
           if (ragged) {
@@ -801,6 +778,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_new = rebase ? m_tile : m;
           const float alpha = rebase ? fast_exp2(m - m_new) : 1.0f;
           const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+          if (C::kOwnP && sc > 0) {
+            // P and O are free again: the previous block's product is done
+            ok = mbar_wait(&bar->pv_done[t], (sc - 1) & 1, abort_flag, p.status);
+            tc_fence_after();
+          }
           float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
           for (int ch = 0; ch < kBK / 32; ++ch) {
@@ -971,21 +953,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------- few rows
 // Items of up to 16 rows: one row of a few sequences over a long prefix, or one
-// sequence's rows over its own keys. The products are too small for a
-// 128-row tensor-memory tile to pay (its softmax keeps one warp busy and its
-// per-item hand-overs cost more than a tail of a few hundred keys), and what bounds
-// the work is reading K and V once. So each warp streams 16 keys (32 at d = 64)
-// from global memory straight into the registers of mma.sync m16n8k16 operands,
-// with 16-byte loads and no shared memory between:
-//   S = Q K^T   the B operand wants pairs along d of one key: lane (g, c) loads
-//               dims (4j + c) 8 .. + 8 of key g. Which d is which k of the
-//               product is free as long as Q's operand uses the same order.
-//   O += P V    the B operand wants pairs along the keys of one column: lane (g, c)
-//               loads dims 8g .. 8g + 8 of keys 2c, 2c+1, 2c+8, 2c+9 and
-//               interleaves them; column g of product t is channel 8g + t.
-// The next step's K is loaded when this step's S is done, its V after O.
-// A CTA's four warps take the steps of a piece in turn and are joined
-// in shared memory at its end.
+// sequence's rows over its own keys. Their products are too small for a
+// 128-row tensor-memory tile to pay: its softmax keeps one warp busy (2.1k cycles a
+// block) and holds a V buffer meanwhile, so that it ran at 3.2k cycles for 64 KB (3.4 TB/s)
+// and took some 20k for a tail of three blocks. What bounds the work is
+// reading K and V once. So one CTA per SM streams them through a ring of
+// 160 KB, across the borders of items, and four warps take 16 keys (32 at d = 64) of each
+// block with mma.sync m16n8k16 (the four joined at the end of a piece):
+// a block's 32 KB take 1.4k cycles from HBM, its products and softmax 0.7k of each warp.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -995,59 +970,155 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ld_stream(const uint4* p) {  // read once: not kept in L1
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
 }
 
-template <int D>
-struct FewCfg {
-  static constexpr int kKeys = 2048 / D;        // keys of a warp's step
-  static constexpr int kUnit = kKeys * kFewWarps;  // keys of a CTA's step: the block of the line
-  static constexpr int kOffQ = 0;               // uint4 [D/32][2][32]: Q in operand order
-  static constexpr int kOffO = kOffQ + D / 32 * 2 * 32 * 16;  // float [warps][16][D]
-  static constexpr int kOffMl = kOffO + kFewWarps * kFewRows * D * 4;
-  static constexpr int kOffBatch = kOffMl + kFewWarps * kFewRows * 8;
-  static constexpr int smem(int B) { return kOffBatch + (B + 1) * 8 + 2 * B * 4; }
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+constexpr int kFewThreads = (kFewWarps + 3) * 32;  // and K, V, and query-row warps
+
+struct FewBarriers {
+  uint64_t item_full[kOrders], item_empty[kOrders];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t sync;
+  int abort_flag;
 };
 
 template <int D>
-__global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
-    prefix_few_kernel(const __grid_constant__ Params p) {
-  using C = FewCfg<D>;
-  constexpr int kThreadsFew = kFewWarps * 32;
-  constexpr int NG = C::kKeys / 16;  // groups of 16 keys (one page each) of a step
-  constexpr int NJ = D / 32;         // 16-byte chunks a lane has of a K row
-  constexpr int NH = D / 64;         // and of a V row
-  extern __shared__ __align__(16) uint8_t few_smem[];
-  uint4* s_q = reinterpret_cast<uint4*>(few_smem + C::kOffQ);
-  float* s_o = reinterpret_cast<float*>(few_smem + C::kOffO);
-  float2* s_ml = reinterpret_cast<float2*>(few_smem + C::kOffMl);
-  const Sizes& z = p.z;
-  int64_t* s_cum = reinterpret_cast<int64_t*>(few_smem + C::kOffBatch);
-  int* s_seq = reinterpret_cast<int*>(s_cum + z.B + 1);
-  int* s_len = s_seq + z.B;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
-  const int g = lane >> 2, c = lane & 3;
+struct FewCfg {
+  static constexpr int kKeys = 2048 / D;           // keys of a block that a warp takes
+  static constexpr int kBlock = kKeys * kFewWarps;
+  static constexpr int kPanel = kBlock * 128;
+  static constexpr int kTile = D / 64 * kPanel;    // 16 KB
+  static constexpr int kStages = 5;
+  static constexpr int kQRow = D * 2 + 16;         // bytes from row to row: no bank conflicts
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kOffO = kOffV + kStages * kTile;  // float [warps][16][D]
+  static constexpr int kOffMl = kOffO + kFewWarps * kFewRows * D * 4;
+  static constexpr int kOffQ = kOffMl + kFewWarps * kFewRows * 8;
+  static constexpr int kOffBar = kOffQ + 2 * kFewRows * kQRow;
+  static constexpr int kOffOrder = kOffBar + 512;
+  static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);
+  static constexpr int kSmem = kOffBatch + (kMaxBatch + 1) * 8 + 2 * kMaxBatch * 4 + 1024;
+  static_assert(sizeof(FewBarriers) <= 512, "barriers");
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
 
+template <int D>
+__global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid_constant__ Params p) {
+  using C = FewCfg<D>;
+  constexpr int NG = C::kKeys / 16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* s_o = reinterpret_cast<float*>(smem + C::kOffO);
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
+  FewBarriers* bar = reinterpret_cast<FewBarriers*>(smem + C::kOffBar);
+  Order* s_order = reinterpret_cast<Order*>(smem + C::kOffOrder);
+  int64_t* s_cum = reinterpret_cast<int64_t*>(smem + C::kOffBatch);
+  int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 1);
+  int* s_len = s_seq + kMaxBatch;
+  volatile int* abort_flag = &bar->abort_flag;
+  const Sizes& z = p.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
+  if (tid == 0) {
+    prefetch_tensormap(&p.tm_k);
+    prefetch_tensormap(&p.tm_v);
+    for (int s = 0; s < kOrders; ++s) {
+      mbar_init(&bar->item_full[s], 1);
+      mbar_init(&bar->item_empty[s], kFewWarps + 2);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bar->q_full[s], 32);
+      mbar_init(&bar->q_empty[s], kFewWarps);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&bar->k_full[s], 1);
+      mbar_init(&bar->k_empty[s], kFewWarps);
+      mbar_init(&bar->v_full[s], 1);
+      mbar_init(&bar->v_empty[s], kFewWarps);
+    }
+    mbar_init(&bar->sync, kFewWarps);
+    bar->abort_flag = 0;
+    fence_mbar_init();
+  }
   int64_t from, to, total;
   int n_pieces;
-  if (!plan_piece<kThreadsFew, C::kUnit>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) return;
-  Walk walk(z, s_cum, from, to);
-  Item it;
-  while (walk.next(it)) {
-    // ---- Q in operand order; rows past the item's are zeros
-    __syncthreads();
-    for (int i = tid; i < NJ * 2 * 32; i += kThreadsFew) {
-      const int r = (i >> 2 & 7) + (i >> 5 & 1) * 8, ch = (i >> 6) * 4 + (i & 3);
-      uint4 x = make_uint4(0, 0, 0, 0);
-      if (r < it.rows) x = reinterpret_cast<const uint4*>(p.q + q_row(z, it, r) * D)[ch];
-      s_q[(i >> 6) * 64 + (i >> 5 & 1) * 32 + (i & 31)] = x;
+  if (!plan_piece<kFewThreads, C::kBlock>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) return;
+  __syncthreads();
+  Orders orders{s_order, bar->item_full, bar->item_empty, abort_flag, p.status};
+
+  if (warp == kFewWarps || warp == kFewWarps + 1) {
+    const bool is_k = warp == kFewWarps;
+    stream_blocks<D, C::kBlock, C::kStages>(p, is_k ? &p.tm_k : &p.tm_v,
+                                            smem + (is_k ? C::kOffK : C::kOffV),
+                                            is_k ? bar->k_full : bar->v_full,
+                                            is_k ? bar->k_empty : bar->v_empty, orders);
+    return;
+  }
+  if (warp == kFewWarps + 2) {
+    // ------------------------------------------------------------ orders and query rows
+    Walk walk(z, s_cum, from, to);
+    Item item;
+    for (int qn = 0;; ++qn) {
+      const bool more = walk.next(item);
+      if (!publish<C::kBlock>(p, orders, more, item, walk, total, n_pieces, s_seq, s_len) || !more)
+        break;
+      const bool ok =
+          mbar_wait(&bar->q_empty[qn & 1], ((qn >> 1) & 1) ^ 1, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int mine = lane < item.rows ? static_cast<int>(q_row(z, item, lane)) : 0;
+      const uint32_t dst = smem_u32(smem + C::kOffQ + (qn & 1) * kFewRows * C::kQRow);
+      constexpr int kVecs = D / 8;
+      for (int i = lane / kVecs; i < kFewRows; i += 32 / kVecs) {
+        const int src = __shfl_sync(0xffffffffu, mine, i);
+        if (i < item.rows)
+          cp_async16(dst + i * C::kQRow + (lane % kVecs) * 16,
+                     p.q + static_cast<int64_t>(src) * D + (lane % kVecs) * 8);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      mbar_arrive(&bar->q_full[qn & 1]);
     }
-    __syncthreads();
+    return;
+  }
+
+  // -------------------------------------------------------------- products and softmax
+  const int g = lane >> 2, c = lane & 3;
+  const uint32_t k_addr = smem_u32(smem + C::kOffK), v_addr = smem_u32(smem + C::kOffV);
+  // This lane's row of the 8 x 8 matrices of a 16 x 16 tile: K as it lies (key, then the
+  // second 8 dims, then the second 8 keys), V to be transposed (second 8 keys first).
+  const int k_key = warp * C::kKeys + (lane & 7) + (lane >> 4) * 8, k_ch = lane >> 3 & 1;
+  const int v_key = warp * C::kKeys + (lane & 7) + (lane >> 3 & 1) * 8, v_ch = lane >> 4;
+  auto at_of = [](int key, int ch) {  // byte of 16-byte chunk `ch` of a key's row in a swizzled tile
+    return (ch >> 3) * C::kPanel + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
+  };
+  int n0 = 0, syncs = 0, items = 0;
+  bool ok = true;
+  auto sync_warps = [&]() {  // the warps that compute; bounded as every wait
+    warp_arrive(&bar->sync);
+    ok = ok && mbar_wait(&bar->sync, syncs++ & 1, abort_flag, p.status);
+  };
+  Order it;
+  for (; orders.take(it); ++items) {
+    uint32_t qa[D / 16][4];  // Q in operand order; rows past the item's hold anything
+    ok = mbar_wait(&bar->q_full[items & 1], (items >> 1) & 1, abort_flag, p.status);
+    if (!ok) break;
+    const uint32_t q_addr = smem_u32(smem + C::kOffQ + (items & 1) * kFewRows * C::kQRow) +
+                            ((lane & 7) + (lane >> 3 & 1) * 8) * C::kQRow + (lane >> 4) * 16;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) ldmatrix4(qa[kk], q_addr + kk * 32);
+    warp_arrive(&bar->q_empty[items & 1]);
 
     float o[D / 8][4];
 #pragma unroll
@@ -1055,71 +1126,17 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};  // rows g and g + 8, log2 units
-
-    // The step of block k: its first key's position and the positions that count.
-    struct Step {
-      int key0, lo, hi;
-      int64_t base[NG];  // row of the pool of each 16 keys; -1: zeros
-    };
-    auto step_of = [&](int k) {
-      const Block b = block_of<C::kUnit>(z, p.prefix_seq, s_seq, s_len, it, k);
-      Step s;
-      s.key0 = b.blk * C::kUnit + warp * C::kKeys;
-      s.lo = b.blk * C::kUnit + b.lo;
-      s.hi = b.blk * C::kUnit + b.hi;
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        const int pos = s.key0 + n * 16;
-        s.base[n] = -1;
-        if (pos < s.hi && pos + 16 > s.lo) {
-          const int page =
-              __ldg(p.table + static_cast<int64_t>(b.seq) * p.c.max_pages + pos / p.c.ps);
-          if (page >= 0 && page < p.c.n_pages) {
-            s.base[n] = (static_cast<int64_t>(page) * p.c.H_kv + it.kv) * p.c.ps + pos % p.c.ps;
-          } else if (lane == 0) {
-            atomicOr(p.status, kDevErrBounds);
-          }
-        }
-      }
-      return s;
-    };
-    uint4 kx[NG][2][NJ], vx[NG][4][NH];
-    auto load_k = [&](const Step& s) {
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int key = n * 16 + u * 8 + g;
-          const bool in = s.base[n] >= 0 && s.key0 + key >= s.lo && s.key0 + key < s.hi;
-          const uint4* src =
-              reinterpret_cast<const uint4*>(p.k_pages + (s.base[n] + u * 8 + g) * D) + c;
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-            kx[n][u][j] = in ? ld_stream(src + j * 4) : make_uint4(0, 0, 0, 0);
-        }
-    };
-    auto load_v = [&](const Step& s) {
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int at = 2 * c + (i & 1) + (i >> 1) * 8;
-          const int key = n * 16 + at;
-          const bool in = s.base[n] >= 0 && s.key0 + key >= s.lo && s.key0 + key < s.hi;
-          const uint4* src = reinterpret_cast<const uint4*>(p.v_pages + (s.base[n] + at) * D) + g;
-#pragma unroll
-          for (int h = 0; h < NH; ++h)
-            vx[n][i][h] = in ? ld_stream(src + h * 8) : make_uint4(0, 0, 0, 0);
-        }
-    };
-
-    Step cur = step_of(it.lo);
-    load_k(cur);
-    load_v(cur);
-    for (int k = it.lo; k < it.hi; ++k) {
-      const bool more = k + 1 < it.hi;
-      Step nxt = cur;
-      if (more) nxt = step_of(k + 1);
+    for (int k = it.lo; k < it.hi; ++k, ++n0) {
+      const int st = n0 % C::kStages, par = (n0 / C::kStages) & 1;
+      // keys of this warp's share that count
+      const int k_lo = (k == it.pre ? it.lo_own : 0) - warp * C::kKeys;
+      const int k_hi = (k == it.pre - 1                    ? it.hi_pre
+                        : k >= it.pre && k == it.nb - 1 ? it.hi_last
+                                                        : C::kBlock) -
+                       warp * C::kKeys;
+      const bool ragged = k_lo > 0 || k_hi < C::kKeys;
+      ok = mbar_wait(&bar->k_full[st], par, abort_flag, p.status);
+      if (!ok) break;
       float s[NG][2][4];
 #pragma unroll
       for (int n = 0; n < NG; ++n)
@@ -1128,26 +1145,24 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][u][e] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const uint4 qa = s_q[j * 64 + lane], qb = s_q[j * 64 + 32 + lane];
+      for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            mma_16816(s[n][u], qa.x, qb.x, qa.y, qb.y, kx[n][u][j].x, kx[n][u][j].y);
-            mma_16816(s[n][u], qa.z, qb.z, qa.w, qb.w, kx[n][u][j].z, kx[n][u][j].w);
-          }
-      }
-      if (more) load_k(nxt);
-      if (cur.key0 < cur.lo || cur.key0 + C::kKeys > cur.hi) {
+        for (int n = 0; n < NG; ++n) {
+          uint32_t b[4];
+          ldmatrix4(b, k_addr + st * C::kTile + at_of(k_key + n * 16, kk * 2 + k_ch));
+          mma_16816(s[n][0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[0], b[1]);
+          mma_16816(s[n][1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[2], b[3]);
+        }
+      warp_arrive(&bar->k_empty[st]);
+      if (ragged) {
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int pos = cur.key0 + n * 16 + u * 8 + 2 * c + (e & 1);
-              if (pos < cur.lo || pos >= cur.hi) s[n][u][e] = -INFINITY;
+              const int key = n * 16 + u * 8 + 2 * c + (e & 1);
+              if (key < k_lo || key >= k_hi) s[n][u][e] = -INFINITY;
             }
       }
       // ---- running maximum and sum of rows g (e = 0, 1) and g + 8 (e = 2, 3)
@@ -1175,9 +1190,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[i][e] *= alpha[e >> 1];
       }
+      uint32_t pa[NG][4];
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        uint32_t pa[4];
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -1185,25 +1200,34 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
             const float e0 = fast_exp2(fmaf(s[n][u][2 * r], p.scale_log2, -base[r]));
             const float e1 = fast_exp2(fmaf(s[n][u][2 * r + 1], p.scale_log2, -base[r]));
             l[r] += e0 + e1;
-            pa[u * 2 + r] = pack_bf16x2(e0, e1);
+            pa[n][u * 2 + r] = pack_bf16x2(e0, e1);
           }
+      ok = mbar_wait(&bar->v_full[st], par, abort_flag, p.status);
+      if (!ok) break;
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-          const uint4 &v0 = vx[n][0][h], &v1 = vx[n][1][h], &v2 = vx[n][2][h], &v3 = vx[n][3][h];
-          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
-          const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
+      for (int n = 0; n < NG; ++n) {
+        // Values that do not count may hold anything, and 0 times NaN is NaN: cleared.
+        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};  // of keys 2c, 2c + 1 and 2c + 8, 2c + 9
+        if (ragged) {
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const uint32_t pick = t & 1 ? 0x7632u : 0x5410u;
-            mma_16816(o[h * 8 + t], pa[0], pa[1], pa[2], pa[3],
-                      __byte_perm(w0[t >> 1], w1[t >> 1], pick),
-                      __byte_perm(w2[t >> 1], w3[t >> 1], pick));
+          for (int u = 0; u < 2; ++u) {
+            const int key = n * 16 + u * 8 + 2 * c;
+            keep[u] = (key >= k_lo && key < k_hi ? 0x0000ffffu : 0u) |
+                      (key + 1 >= k_lo && key + 1 < k_hi ? 0xffff0000u : 0u);
           }
         }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          uint32_t b[4];
+          ldmatrix4_trans(b, v_addr + st * C::kTile + at_of(v_key + n * 16, i * 2 + v_ch));
+          if (ragged) b[0] &= keep[0], b[1] &= keep[1], b[2] &= keep[0], b[3] &= keep[1];
+          mma_16816(o[2 * i], pa[n][0], pa[n][1], pa[n][2], pa[n][3], b[0], b[1]);
+          mma_16816(o[2 * i + 1], pa[n][0], pa[n][1], pa[n][2], pa[n][3], b[2], b[3]);
+        }
       }
-      if (more) load_v(nxt);
-      cur = nxt;
+      warp_arrive(&bar->v_empty[st]);
     }
+    if (!ok) break;
 
     // ---- the four warps' (O, m, l) joined
 #pragma unroll
@@ -1212,7 +1236,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       if (c == 0) s_ml[warp * kFewRows + g + 8 * r] = make_float2(m[r], l[r]);
     }
-    __syncthreads();
+    sync_warps();
+    if (!ok) break;
     float f[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -1221,25 +1246,22 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
       for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, s_ml[w * kFewRows + g + 8 * r].x);
       f[r] = fast_exp2(m[r] - (top == -INFINITY ? 0.0f : top));
     }
-    // a lane has channels 8 (8h + 2c) .. + 16 of its rows
 #pragma unroll
-    for (int h = 0; h < NH; ++h)
+    for (int r = 0; r < 2; ++r) {
+      if (g + 8 * r >= it.rows) continue;
+      float* dst = s_o + (warp * kFewRows + g + 8 * r) * D + 2 * c;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (g + 8 * (e >> 1) >= it.rows) continue;
-        float* dst = s_o + (warp * kFewRows + g + 8 * (e >> 1)) * D + (h * 8 + 2 * c + (e & 1)) * 8;
-#pragma unroll
-        for (int t = 0; t < 8; t += 4)
-          *reinterpret_cast<float4*>(dst + t) =
-              make_float4(o[h * 8 + t][e] * f[e >> 1], o[h * 8 + t + 1][e] * f[e >> 1],
-                          o[h * 8 + t + 2][e] * f[e >> 1], o[h * 8 + t + 3][e] * f[e >> 1]);
-      }
-    __syncthreads();
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<float2*>(dst + i * 8) =
+            make_float2(o[i][2 * r] * f[r], o[i][2 * r + 1] * f[r]);
+    }
+    sync_warps();
+    if (!ok) break;
     const Pieces& part = p.part[it.shared ? 0 : 1];
-    const int64_t slot = slot_of(p, it) * part.stride;
+    const int64_t slot = static_cast<int64_t>(it.lo > 0 ? blockIdx.x : it.id) * part.stride;
     float4* out = (it.lo > 0 ? part.head_o : part.first_o) + slot * (D / 4);
     float2* out_ml = (it.lo > 0 ? part.head_ml : part.first_ml) + slot;
-    for (int i = tid; i < it.rows * (D / 4); i += kThreadsFew) {
+    for (int i = tid; i < it.rows * (D / 4); i += kFewWarps * 32) {
       const int r = i / (D / 4), ch = i % (D / 4);
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -1259,7 +1281,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, kFewPerSm)
         out_ml[r] = make_float2(top, sum);
       }
     }
-    if (tid == 0 && it.lo == 0) part.info[it.id] = pieces_of(it, walk.at, total, n_pieces);
+    if (tid == 0 && it.lo == 0) part.info[it.id] = make_int2(blockIdx.x, it.pieces);
+    sync_warps();  // s_o and s_ml are free again
+    if (!ok) break;
   }
 }
 
@@ -1427,7 +1451,7 @@ Layout layout(const CacheDims& c, int32_t B, int32_t H, int32_t Lq, Form form) {
     // tile slots hold whole warps of rows, so that a warp's stores are whole lines
     t.stride = few ? all : all < kGroup ? (all + 31) / 32 * 32 : kGroup;
     const size_t items = static_cast<size_t>(c.H_kv) * (i == 0 ? 1 : B) * t.groups;
-    const size_t heads = static_cast<size_t>(few ? kFewCtas : kMaxCtas) * t.stride;
+    const size_t heads = static_cast<size_t>(kMaxCtas) * t.stride;
     const size_t firsts = form == kJoint ? heads : items * t.stride;
     t.info = take(items * sizeof(int2));
     t.first_o = take(firsts * c.d * sizeof(float));
@@ -1480,22 +1504,32 @@ template <int D>
 cudaError_t launch_few(const Params& p, cudaStream_t stream) {
   using C = FewCfg<D>;
   auto kern = prefix_few_kernel<D>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       C::smem(kMaxBatch));
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<p.z.n_ctas, kFewWarps * 32, C::smem(p.z.B), stream>>>(p);
+  kern<<<p.z.n_ctas, kFewThreads, C::kSmem, stream>>>(p);
   return cudaGetLastError();
+}
+
+// Maps of the pools in boxes of the rows of a page, or of a block where that is less.
+bool set_maps(const PrefixArgs& a, Params& p, int bk) {
+  const int32_t pool_rows = a.c.n_pages * a.c.H_kv * a.c.ps;
+  const int box = a.c.ps < bk ? a.c.ps : bk;
+  return make_tmap_bf16(&p.tm_k, a.k_pages, a.c.d, pool_rows, 1, box) &&
+         make_tmap_bf16(&p.tm_v, a.v_pages, a.c.d, pool_rows, 1, box);
 }
 
 template <int D>
 cudaError_t launch(const PrefixArgs& a, Params& p, Form form, int sms, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (form == kFew || form == kMixed) {
-    p.z = sizes_of(a, sms * kFewPerSm, true, form == kFew, true, false);
+    p.z = sizes_of(a, sms, true, form == kFew, true, false);
+    if (!set_maps(a, p, FewCfg<D>::kBlock)) return cudaErrorInvalidValue;
     if ((e = launch_few<D>(p, stream)) != cudaSuccess) return e;
   }
   if (form != kFew) {
     p.z = sizes_of(a, sms, false, form != kJoint, form != kMixed, form == kJoint);
+    if (!set_maps(a, p, kBK) || !make_tmap_bf16(&p.tm_q, a.q, D, a.B * a.H * a.Lq, 1, 128))
+      return cudaErrorInvalidValue;
     if ((e = launch_tiles<D>(p, stream)) != cudaSuccess) return e;
   }
   if (form == kJoint) {
@@ -1528,14 +1562,6 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int* status, cudaStream
   memset(&p, 0, sizeof(p));
   const int GL = a.H / a.c.H_kv * a.Lq;
   const Form form = form_of(a.B, GL, a.prefix_len > 0);
-  if (form != kFew) {
-    const int32_t pool_rows = a.c.n_pages * a.c.H_kv * a.c.ps;
-    const int box = a.c.ps < kBK ? a.c.ps : kBK;
-    if (!make_tmap_bf16(&p.tm_k, a.k_pages, a.c.d, pool_rows, 1, box) ||
-        !make_tmap_bf16(&p.tm_v, a.v_pages, a.c.d, pool_rows, 1, box) ||
-        !make_tmap_bf16(&p.tm_q, a.q, a.c.d, a.B * a.H * a.Lq, 1, 128))
-      return cudaErrorInvalidValue;
-  }
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
