@@ -151,6 +151,9 @@ CASES = {
     "batch_1024": (1024, 1, 1, 64, 16, 33, 1, [i % 3 for i in range(1024)]),
     "one_sequence": (1, 8, 2, 128, 64, 1000, 5, [5]),
     "heads_40": (2, 40, 40, 64, 16, 90, 1, [3, 20]),
+    # several long items to every CTA
+    "long_tails_of_many": (12, 24, 24, 64, 64, 300, 1, [900 + 97 * i for i in range(12)]),
+    "long_tails_of_rows": (12, 24, 12, 128, 128, 700, 20, [600 + 97 * i for i in range(12)]),
 }
 
 

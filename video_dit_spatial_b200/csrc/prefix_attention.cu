@@ -55,7 +55,7 @@ constexpr int kGroup = 256;          // rows of an item
 constexpr int kMaxCtas = 148;
 constexpr int kMaxBatch = 1024;
 constexpr int kFewRows = 16;    // rows of an item of the few-row kernel
-constexpr int kFewWarps = 4;    // of them that compute
+constexpr int kFewWarps = 4;    // that compute
 // Cost of a block: a two-tile block keeps the tensor core and the exponentials
 // busy for about 3.7k cycles, a one-tile block takes about as long as its
 // 64 KB take from HBM on every SM at once, 2.8k.
@@ -70,6 +70,8 @@ struct Sizes {
   int32_t prefix_len, nbp;       // blocks of the prefix
   int32_t groups_p, groups_s;    // row groups of a shared item's key head, of a sequence
   int32_t cost_p, cost_s;        // cost of one block over all those groups
+  int64_t shared_cost;           // of all shared items, also where another kernel has them
+  int32_t mixed;                 // 1: the other kind of items is another kernel's, at the same time
 };
 
 __host__ __device__ inline int rows_of(int total, int g, int group) {
@@ -177,6 +179,35 @@ struct Cfg {
   static constexpr int kUsed = kOffBatch + (kMaxBatch + 1) * 8 + 2 * kMaxBatch * 4 + 1024;
   static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA per SM
   static_assert(sizeof(Barriers) <= 512, "barriers");
+  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+
+struct FewBarriers {
+  uint64_t item_full[kOrders], item_empty[kOrders];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
+  uint64_t sync;
+  int abort_flag;
+};
+
+template <int D>
+struct FewCfg {
+  static constexpr int kKeys = 2048 / D;           // keys of a block that a warp takes
+  static constexpr int kBlock = kKeys * kFewWarps;
+  static constexpr int kPanel = kBlock * 128;
+  static constexpr int kTile = D / 64 * kPanel;    // 16 KB
+  static constexpr int kStages = 5;
+  static constexpr int kQRow = D * 2 + 16;         // bytes from row to row: no bank conflicts
+  static constexpr int kOffK = 0;
+  static constexpr int kOffV = kOffK + kStages * kTile;
+  static constexpr int kOffO = kOffV + kStages * kTile;  // float [warps][16][D]
+  static constexpr int kOffMl = kOffO + kFewWarps * kFewRows * D * 4;
+  static constexpr int kOffQ = kOffMl + kFewWarps * kFewRows * 8;
+  static constexpr int kOffBar = kOffQ + 2 * kFewRows * kQRow;
+  static constexpr int kOffOrder = kOffBar + 512;
+  static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);
+  static constexpr int kSmem = kOffBatch + (kMaxBatch + 1) * 8 + 2 * kMaxBatch * 4 + 1024;
+  static_assert(sizeof(FewBarriers) <= 512, "barriers");
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
 
@@ -300,10 +331,10 @@ __device__ __forceinline__ int64_t q_row(const Sizes& z, const Item& it, int r) 
 
 // No piece is smaller than a block, so that every CTA from an item's first to
 // its last has a piece of it.
-__device__ __forceinline__ bool cut_piece(const Sizes& z, int64_t total, int64_t& from, int64_t& to,
+__device__ __forceinline__ bool cut_piece(int n_ctas, int64_t total, int64_t& from, int64_t& to,
                                           int& n_pieces) {
   const int64_t most = total / kCostTwo < 1 ? 1 : total / kCostTwo;
-  n_pieces = static_cast<int>(most < z.n_ctas ? most : z.n_ctas);
+  n_pieces = static_cast<int>(most < n_ctas ? most : n_ctas);
   const int cta = blockIdx.x;
   if (cta >= n_pieces || total == 0) return false;
   from = total * cta / n_pieces;
@@ -311,19 +342,28 @@ __device__ __forceinline__ bool cut_piece(const Sizes& z, int64_t total, int64_t
   return true;
 }
 
+// SMs that the few-row kernel takes of n while the tile kernel has the rest: as the
+// cycles of their work, some 1500 for one of its blocks (an item's beginning and
+// end among them) and 1000 for a unit of the tile kernel's cost. Both kernels are
+// launched with n CTAs and those past their share leave at once, since the lengths
+// are not known on the host. At d = 128, one kernel after the other and side by
+// side: rows of 64 sequences over 20001 shared rows and up to 700 of their own,
+// four query heads to a key head, 79 and 71 us; of 200 over 30000 and up to 300, eight, 90 and 87 us.
+__device__ __forceinline__ int few_share(int n, int64_t few_blocks, int64_t tile_cost) {
+  if (few_blocks == 0) return 0;
+  const int64_t s = n * 3 * few_blocks / (3 * few_blocks + 2 * tile_cost);
+  return s < 1 ? 1 : s > n - 1 ? n - 1 : static_cast<int>(s);
+}
+
 // The batch's lengths into shared memory and this CTA's piece [from, to) of the
 // line of cost; false: it has none. Every CTA finds the same line.
-template <int T, int BK>
+template <int T, int BK, int FEW_BK>
 __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int* s_seq, int* s_len,
                                            int64_t& from, int64_t& to, int64_t& total,
                                            int& n_pieces) {
   const Sizes& z = p.z;
   const int tid = threadIdx.x, cta = blockIdx.x;
   const bool ok_prefix = prefix_ok(p.c, p.lens, p.prefix_seq, z.prefix_len);
-  if (!z.own) {  // no sequence's own keys: the shared items alone
-    total = ok_prefix ? static_cast<int64_t>(z.nbp) * z.cost_p * z.H_kv : 0;
-    return cut_piece(z, total, from, to, n_pieces);
-  }
   for (int b = tid; b < z.B; b += T) {
     const int seq = p.seqs[b];
     const int len = entry_len(p.c, p.lens, seq);
@@ -332,7 +372,7 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
     s_len[b] = len;
     s_cum[b + 1] = len < 0 || !ok_prefix
                        ? 0
-                       : own_blocks(len, z.prefix_len, BK) + (z.joint ? z.nbp : 0);
+                       : own_blocks(len, z.prefix_len, z.own ? BK : FEW_BK) + (z.joint ? z.nbp : 0);
   }
   __syncthreads();
   if (tid < 32) {
@@ -351,9 +391,15 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
     if (tid == 0) s_cum[0] = 0;
   }
   __syncthreads();
-  total = s_cum[z.B] * z.cost_s * z.H_kv;
-  if (z.shared && ok_prefix) total += static_cast<int64_t>(z.nbp) * z.cost_p * z.H_kv;
-  return cut_piece(z, total, from, to, n_pieces);
+  const int64_t own = s_cum[z.B] * z.H_kv;  // blocks, of one group of rows each
+  const int64_t shared = ok_prefix ? z.shared_cost : 0;
+  int n = z.n_ctas;
+  if (z.mixed) {
+    const int few = few_share(n, own, shared);
+    n = z.own ? few : n - few;
+  }
+  total = (z.own ? own * z.cost_s : 0) + (z.shared ? shared : 0);
+  return cut_piece(n, total, from, to, n_pieces);
 }
 
 // First CTA (this one) and number of pieces of the item whose first block it has.
@@ -494,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Sizes& z = p.z;
   const int tid = threadIdx.x, warp = tid >> 5;
   const int cta = blockIdx.x;
+  launch_dependents();  // the join waits for this kernel's end by itself
   if (tid == 0) {
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
@@ -502,8 +549,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   int64_t from, to, total;
   int n_pieces;
-  if (!plan_piece<kThreads, kBK>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) {
+  if (!plan_piece<kThreads, kBK, FewCfg<D>::kBlock>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) {
     if (z.joint && tid == 0) p.head_item[cta] = -1;
+    if (tid == 0) wait_for_primary();
     return;
   }
 
@@ -743,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool ragged = k_lo > 0 || k_hi < kBK;
         ok = mbar_wait(&bar->s_full[t], sc & 1, abort_flag, p.status);
         if (!ok) break;
+        __syncwarp();
         tc_fence_after();
         uint32_t sr[kBK];
         if (active) {
@@ -781,6 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (C::kOwnP && sc > 0) {
             // P and O are free again: the previous block's product is done
             ok = mbar_wait(&bar->pv_done[t], (sc - 1) & 1, abort_flag, p.status);
+            __syncwarp();
             tc_fence_after();
           }
           float s0 = 0.0f, s1 = 0.0f;
@@ -868,6 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fp ^= both ? 3u : 1u;
       }
       if (!ok) break;
+      __syncwarp();
       tc_fence_after();
       const int rr = two ? t * 128 + r : r;  // row of the item
       const bool valid = r < rows;
@@ -949,6 +1000,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  // This kernel needs nothing of the few-row kernel before it, but the join, which
+  // waits for this one, needs both to have ended.
+  if (tid == 0) wait_for_primary();
 }
 
 // ---------------------------------------------------------------- few rows
@@ -960,7 +1014,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // reading K and V once. So one CTA per SM streams them through a ring of
 // 160 KB, across the borders of items, and four warps take 16 keys (32 at d = 64) of each
 // block with mma.sync m16n8k16 (the four joined at the end of a piece):
-// a block's 32 KB take 1.4k cycles from HBM, its products and softmax 0.7k of each warp.
+// a block's 32 KB take 1.4k cycles from HBM, its products and softmax some 0.9k of each warp.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -986,35 +1040,6 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
 
 constexpr int kFewThreads = (kFewWarps + 3) * 32;  // and K, V, and query-row warps
 
-struct FewBarriers {
-  uint64_t item_full[kOrders], item_empty[kOrders];
-  uint64_t q_full[2], q_empty[2];
-  uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
-  uint64_t sync;
-  int abort_flag;
-};
-
-template <int D>
-struct FewCfg {
-  static constexpr int kKeys = 2048 / D;           // keys of a block that a warp takes
-  static constexpr int kBlock = kKeys * kFewWarps;
-  static constexpr int kPanel = kBlock * 128;
-  static constexpr int kTile = D / 64 * kPanel;    // 16 KB
-  static constexpr int kStages = 5;
-  static constexpr int kQRow = D * 2 + 16;         // bytes from row to row: no bank conflicts
-  static constexpr int kOffK = 0;
-  static constexpr int kOffV = kOffK + kStages * kTile;
-  static constexpr int kOffO = kOffV + kStages * kTile;  // float [warps][16][D]
-  static constexpr int kOffMl = kOffO + kFewWarps * kFewRows * D * 4;
-  static constexpr int kOffQ = kOffMl + kFewWarps * kFewRows * 8;
-  static constexpr int kOffBar = kOffQ + 2 * kFewRows * kQRow;
-  static constexpr int kOffOrder = kOffBar + 512;
-  static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);
-  static constexpr int kSmem = kOffBatch + (kMaxBatch + 1) * 8 + 2 * kMaxBatch * 4 + 1024;
-  static_assert(sizeof(FewBarriers) <= 512, "barriers");
-  static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-};
-
 template <int D>
 __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid_constant__ Params p) {
   using C = FewCfg<D>;
@@ -1022,8 +1047,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* s_o = reinterpret_cast<float*>(smem + C::kOffO);
-  float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   FewBarriers* bar = reinterpret_cast<FewBarriers*>(smem + C::kOffBar);
   Order* s_order = reinterpret_cast<Order*>(smem + C::kOffOrder);
   int64_t* s_cum = reinterpret_cast<int64_t*>(smem + C::kOffBatch);
@@ -1032,6 +1055,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   volatile int* abort_flag = &bar->abort_flag;
   const Sizes& z = p.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = lane_id();
+  launch_dependents();
   if (tid == 0) {
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
@@ -1055,7 +1079,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   }
   int64_t from, to, total;
   int n_pieces;
-  if (!plan_piece<kFewThreads, C::kBlock>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) return;
+  if (!plan_piece<kFewThreads, C::kBlock, C::kBlock>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) return;
   __syncthreads();
   Orders orders{s_order, bar->item_full, bar->item_empty, abort_flag, p.status};
 
@@ -1094,12 +1118,15 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   }
 
   // -------------------------------------------------------------- products and softmax
+  const int w = warp;
+  float* s_o = reinterpret_cast<float*>(smem + C::kOffO);
+  float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   const int g = lane >> 2, c = lane & 3;
   const uint32_t k_addr = smem_u32(smem + C::kOffK), v_addr = smem_u32(smem + C::kOffV);
   // This lane's row of the 8 x 8 matrices of a 16 x 16 tile: K as it lies (key, then the
   // second 8 dims, then the second 8 keys), V to be transposed (second 8 keys first).
-  const int k_key = warp * C::kKeys + (lane & 7) + (lane >> 4) * 8, k_ch = lane >> 3 & 1;
-  const int v_key = warp * C::kKeys + (lane & 7) + (lane >> 3 & 1) * 8, v_ch = lane >> 4;
+  const int k_key = w * C::kKeys + (lane & 7) + (lane >> 4) * 8, k_ch = lane >> 3 & 1;
+  const int v_key = w * C::kKeys + (lane & 7) + (lane >> 3 & 1) * 8, v_ch = lane >> 4;
   auto at_of = [](int key, int ch) {  // byte of 16-byte chunk `ch` of a key's row in a swizzled tile
     return (ch >> 3) * C::kPanel + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
   };
@@ -1108,12 +1135,14 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   auto sync_warps = [&]() {  // the warps that compute; bounded as every wait
     warp_arrive(&bar->sync);
     ok = ok && mbar_wait(&bar->sync, syncs++ & 1, abort_flag, p.status);
+    __syncwarp();
   };
   Order it;
   for (; orders.take(it); ++items) {
     uint32_t qa[D / 16][4];  // Q in operand order; rows past the item's hold anything
     ok = mbar_wait(&bar->q_full[items & 1], (items >> 1) & 1, abort_flag, p.status);
     if (!ok) break;
+    __syncwarp();
     const uint32_t q_addr = smem_u32(smem + C::kOffQ + (items & 1) * kFewRows * C::kQRow) +
                             ((lane & 7) + (lane >> 3 & 1) * 8) * C::kQRow + (lane >> 4) * 16;
 #pragma unroll
@@ -1129,30 +1158,37 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
     for (int k = it.lo; k < it.hi; ++k, ++n0) {
       const int st = n0 % C::kStages, par = (n0 / C::kStages) & 1;
       // keys of this warp's share that count
-      const int k_lo = (k == it.pre ? it.lo_own : 0) - warp * C::kKeys;
+      const int k_lo = (k == it.pre ? it.lo_own : 0) - w * C::kKeys;
       const int k_hi = (k == it.pre - 1                    ? it.hi_pre
                         : k >= it.pre && k == it.nb - 1 ? it.hi_last
                                                         : C::kBlock) -
-                       warp * C::kKeys;
+                       w * C::kKeys;
       const bool ragged = k_lo > 0 || k_hi < C::kKeys;
       ok = mbar_wait(&bar->k_full[st], par, abort_flag, p.status);
       if (!ok) break;
-      float s[NG][2][4];
+      __syncwarp();
+      float s[NG][2][4], s2[NG][2][4];  // two chains of products each
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[n][u][e] = 0.0f;
+          for (int e = 0; e < 4; ++e) s[n][u][e] = s2[n][u][e] = 0.0f;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
           uint32_t b[4];
           ldmatrix4(b, k_addr + st * C::kTile + at_of(k_key + n * 16, kk * 2 + k_ch));
-          mma_16816(s[n][0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[0], b[1]);
-          mma_16816(s[n][1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[2], b[3]);
+          mma_16816((kk & 1 ? s2 : s)[n][0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[0], b[1]);
+          mma_16816((kk & 1 ? s2 : s)[n][1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[2], b[3]);
         }
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[n][u][e] += s2[n][u][e];
       warp_arrive(&bar->k_empty[st]);
       if (ragged) {
 #pragma unroll
@@ -1204,6 +1240,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
           }
       ok = mbar_wait(&bar->v_full[st], par, abort_flag, p.status);
       if (!ok) break;
+      __syncwarp();
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         // Values that do not count may hold anything, and 0 times NaN is NaN: cleared.
@@ -1234,7 +1271,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (c == 0) s_ml[warp * kFewRows + g + 8 * r] = make_float2(m[r], l[r]);
+      if (c == 0) s_ml[w * kFewRows + g + 8 * r] = make_float2(m[r], l[r]);
     }
     sync_warps();
     if (!ok) break;
@@ -1243,13 +1280,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
     for (int r = 0; r < 2; ++r) {
       float top = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, s_ml[w * kFewRows + g + 8 * r].x);
+      for (int x = 0; x < kFewWarps; ++x) top = fmaxf(top, s_ml[x * kFewRows + g + 8 * r].x);
       f[r] = fast_exp2(m[r] - (top == -INFINITY ? 0.0f : top));
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       if (g + 8 * r >= it.rows) continue;
-      float* dst = s_o + (warp * kFewRows + g + 8 * r) * D + 2 * c;
+      float* dst = s_o + (w * kFewRows + g + 8 * r) * D + 2 * c;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         *reinterpret_cast<float2*>(dst + i * 8) =
@@ -1265,19 +1302,19 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
       const int r = i / (D / 4), ch = i % (D / 4);
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kFewWarps; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(s_o + (w * kFewRows + r) * D + ch * 4);
+      for (int i4 = 0; i4 < kFewWarps; ++i4) {
+        const float4 y = *reinterpret_cast<const float4*>(s_o + (i4 * kFewRows + r) * D + ch * 4);
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
       }
       out[i] = x;
       if (ch == 0) {
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w) top = fmaxf(top, s_ml[w * kFewRows + r].x);
+        for (int x = 0; x < kFewWarps; ++x) top = fmaxf(top, s_ml[x * kFewRows + r].x);
 #pragma unroll
-        for (int w = 0; w < kFewWarps; ++w)
-          sum += s_ml[w * kFewRows + r].y *
-                 fast_exp2(s_ml[w * kFewRows + r].x - (top == -INFINITY ? 0.0f : top));
+        for (int x4 = 0; x4 < kFewWarps; ++x4)
+          sum += s_ml[x4 * kFewRows + r].y *
+                 fast_exp2(s_ml[x4 * kFewRows + r].x - (top == -INFINITY ? 0.0f : top));
         out_ml[r] = make_float2(top, sum);
       }
     }
@@ -1320,7 +1357,7 @@ __device__ __forceinline__ void store_row(const Params& p, int64_t row, int c4, 
 template <int D>
 __device__ __forceinline__ void join_pieces(Joined& s, const Pieces& part, int2 info,
                                             int64_t first_slot, int r, int c4, int first, int step) {
-#pragma unroll 4
+#pragma unroll 8
   for (int k = first; k < info.y; k += step) {
     const int64_t slot = (k == 0 ? first_slot : info.x + k) * part.stride;
     join_one(s, (k == 0 ? part.first_ml : part.head_ml)[slot + r],
@@ -1340,6 +1377,7 @@ __global__ void __launch_bounds__(D * 2 * F) join_rows_kernel(const __grid_const
   const int64_t row = blockIdx.x * static_cast<int64_t>(8) + (lane >> 2);
   const int c4 = chunk * 4 + (lane & 3);
   Joined s{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  wait_for_primary();
   bool live = row < rows;
   if (live) {
     const int64_t bk = row / z.GL;
@@ -1377,6 +1415,7 @@ __global__ void __launch_bounds__(D * 2) join_cuts_kernel(const __grid_constant_
   const int lane = lane_id();
   const int c4 = (threadIdx.x >> 5) * 4 + (lane & 3);
   Joined s{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+  wait_for_primary();
   if (blockIdx.x == 0) {
     if (z.prefix_len > 0) return;
     const int64_t per = static_cast<int64_t>(z.H_kv) * z.GL;
@@ -1463,8 +1502,8 @@ Layout layout(const CacheDims& c, int32_t B, int32_t H, int32_t Lq, Form form) {
   return l;
 }
 
-// The sizes of the line of one kernel: `few` of them in blocks and groups.
-Sizes sizes_of(const PrefixArgs& a, int n_ctas, bool few, bool shared, bool own, bool joint) {
+// The sizes of one kernel's line: the few-row kernel's or the tile kernel's.
+Sizes sizes_of(const PrefixArgs& a, int n_ctas, bool few, Form form) {
   const int GL = a.H / a.c.H_kv * a.Lq;
   const int bk = few ? kFewWarps * 2048 / a.c.d : kBK, group = few ? kFewRows : kGroup;
   Sizes z;
@@ -1474,20 +1513,42 @@ Sizes sizes_of(const PrefixArgs& a, int n_ctas, bool few, bool shared, bool own,
   z.H_kv = a.c.H_kv;
   z.GL = GL;
   z.group = group;
-  z.shared = shared && a.prefix_len > 0;
-  z.own = own;
-  z.joint = joint;
+  z.mixed = form == kMixed;
+  z.shared = a.prefix_len > 0 && form != kJoint && !(few && form == kMixed);
+  z.own = few || form != kMixed;
+  z.joint = form == kJoint;
   z.prefix_len = a.prefix_len;
   z.nbp = (a.prefix_len + bk - 1) / bk;
   z.groups_p = groups(a.B * GL, group);
   z.groups_s = groups(GL, group);
   z.cost_p = group_cost(a.B * GL, group);
   z.cost_s = group_cost(GL, group);
+  // the tile kernel's, but where the few-row kernel has all
+  z.shared_cost = form == kFew ? static_cast<int64_t>(z.nbp) * z.cost_p * z.H_kv
+                               : static_cast<int64_t>((a.prefix_len + kBK - 1) / kBK) *
+                                     group_cost(a.B * GL, kGroup) * z.H_kv;
   return z;
 }
 
+// `after`: behind a kernel of the same call, whose end the kernel waits for itself.
+template <typename K>
+cudaError_t launch_kernel(K kern, dim3 grid, int threads, int smem, bool after, const Params& p,
+                          cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = after ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
 template <int D>
-cudaError_t launch_tiles(const Params& p, cudaStream_t stream) {
+cudaError_t launch_tiles(const Params& p, bool after, cudaStream_t stream) {
   using C = Cfg<D>;
   auto kern = prefix_attention_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
@@ -1496,8 +1557,7 @@ cudaError_t launch_tiles(const Params& p, cudaStream_t stream) {
   cudaFuncAttributes fa;
   if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
   if (fa.numRegs != kLaunchRegs) return cudaErrorNotSupported;
-  kern<<<p.z.n_ctas, kThreads, C::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(kern, dim3(p.z.n_ctas), kThreads, C::kSmem, after, p, stream);
 }
 
 template <int D>
@@ -1506,8 +1566,7 @@ cudaError_t launch_few(const Params& p, cudaStream_t stream) {
   auto kern = prefix_few_kernel<D>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kern<<<p.z.n_ctas, kFewThreads, C::kSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(kern, dim3(p.z.n_ctas), kFewThreads, C::kSmem, false, p, stream);
 }
 
 // Maps of the pools in boxes of the rows of a page, or of a block where that is less.
@@ -1522,30 +1581,24 @@ template <int D>
 cudaError_t launch(const PrefixArgs& a, Params& p, Form form, int sms, cudaStream_t stream) {
   cudaError_t e = cudaSuccess;
   if (form == kFew || form == kMixed) {
-    p.z = sizes_of(a, sms, true, form == kFew, true, false);
+    p.z = sizes_of(a, sms, true, form);
     if (!set_maps(a, p, FewCfg<D>::kBlock)) return cudaErrorInvalidValue;
     if ((e = launch_few<D>(p, stream)) != cudaSuccess) return e;
   }
   if (form != kFew) {
-    p.z = sizes_of(a, sms, false, form != kJoint, form != kMixed, form == kJoint);
+    p.z = sizes_of(a, sms, false, form);
     if (!set_maps(a, p, kBK) || !make_tmap_bf16(&p.tm_q, a.q, D, a.B * a.H * a.Lq, 1, 128))
       return cudaErrorInvalidValue;
-    if ((e = launch_tiles<D>(p, stream)) != cudaSuccess) return e;
+    if ((e = launch_tiles<D>(p, form == kMixed, stream)) != cudaSuccess) return e;
   }
-  if (form == kJoint) {
-    join_cuts_kernel<D><<<dim3(p.z.n_ctas, kGroup / 8), D * 2, 0, stream>>>(p);
-  } else {
-    // One row's pieces in turn, or by four warps where there are few rows and so
-    // many pieces of each.
-    const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.Lq;
-    const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-    if (grid >= 148) {
-      join_rows_kernel<D, 1><<<grid, D * 2, 0, stream>>>(p);
-    } else {
-      join_rows_kernel<D, 4><<<grid, D * 8, 0, stream>>>(p);
-    }
-  }
-  return cudaGetLastError();
+  if (form == kJoint)
+    return launch_kernel(join_cuts_kernel<D>, dim3(p.z.n_ctas, kGroup / 8), D * 2, 0, true, p, stream);
+  // One row's pieces in turn, or by four warps where there are few rows and so
+  // many pieces of each.
+  const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.Lq;
+  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  if (grid >= 148) return launch_kernel(join_rows_kernel<D, 1>, dim3(grid), D * 2, 0, true, p, stream);
+  return launch_kernel(join_rows_kernel<D, 4>, dim3(grid), D * 8, 0, true, p, stream);
 }
 
 }  // namespace
