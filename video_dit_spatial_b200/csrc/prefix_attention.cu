@@ -196,13 +196,13 @@ struct FewCfg {
   static constexpr int kBlock = kKeys * kFewWarps;
   static constexpr int kPanel = kBlock * 128;
   static constexpr int kTile = D / 64 * kPanel;    // 16 KB
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 4;
   static constexpr int kQRow = D * 2 + 16;         // bytes from row to row: no bank conflicts
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kStages * kTile;
-  static constexpr int kOffO = kOffV + kStages * kTile;  // float [warps][16][D]
-  static constexpr int kOffMl = kOffO + kFewWarps * kFewRows * D * 4;
-  static constexpr int kOffQ = kOffMl + kFewWarps * kFewRows * 8;
+  static constexpr int kOffO = kOffV + kStages * kTile;  // float [2][warps][16][D], by turns
+  static constexpr int kOffMl = kOffO + 2 * kFewWarps * kFewRows * D * 4;
+  static constexpr int kOffQ = kOffMl + 2 * kFewWarps * kFewRows * 8;
   static constexpr int kOffBar = kOffQ + 2 * kFewRows * kQRow;
   static constexpr int kOffOrder = kOffBar + 512;
   static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);
@@ -1012,7 +1012,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // block) and holds a V buffer meanwhile, so that it ran at 3.2k cycles for 64 KB (3.4 TB/s)
 // and took some 20k for a tail of three blocks. What bounds the work is
 // reading K and V once. So one CTA per SM streams them through a ring of
-// 160 KB, across the borders of items, and four warps take 16 keys (32 at d = 64) of each
+// 128 KB, across the borders of items, and four warps take 16 keys (32 at d = 64) of each
 // block with mma.sync m16n8k16 (the four joined at the end of a piece):
 // a block's 32 KB take 1.4k cycles from HBM, its products and softmax some 0.9k of each warp.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -1119,8 +1119,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
 
   // -------------------------------------------------------------- products and softmax
   const int w = warp;
-  float* s_o = reinterpret_cast<float*>(smem + C::kOffO);
-  float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl);
   const int g = lane >> 2, c = lane & 3;
   const uint32_t k_addr = smem_u32(smem + C::kOffK), v_addr = smem_u32(smem + C::kOffV);
   // This lane's row of the 8 x 8 matrices of a 16 x 16 tile: K as it lies (key, then the
@@ -1130,13 +1128,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   auto at_of = [](int key, int ch) {  // byte of 16-byte chunk `ch` of a key's row in a swizzled tile
     return (ch >> 3) * C::kPanel + key * 128 + (((ch & 7) ^ (key & 7)) << 4);
   };
-  int n0 = 0, syncs = 0, items = 0;
+  int n0 = 0, items = 0;
   bool ok = true;
-  auto sync_warps = [&]() {  // the warps that compute; bounded as every wait
-    warp_arrive(&bar->sync);
-    ok = ok && mbar_wait(&bar->sync, syncs++ & 1, abort_flag, p.status);
-    __syncwarp();
-  };
   Order it;
   for (; orders.take(it); ++items) {
     uint32_t qa[D / 16][4];  // Q in operand order; rows past the item's hold anything
@@ -1266,33 +1259,24 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
     }
     if (!ok) break;
 
-    // ---- the four warps' (O, m, l) joined
+    // ---- the four warps' (O, m, l) joined; in places by turns, so that one meeting
+    // of the warps an item is enough: whoever writes a place again has met
+    // the others after they read it
+    float* s_o = reinterpret_cast<float*>(smem + C::kOffO) + (items & 1) * kFewWarps * kFewRows * D;
+    float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl) + (items & 1) * kFewWarps * kFewRows;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (c == 0) s_ml[w * kFewRows + g + 8 * r] = make_float2(m[r], l[r]);
-    }
-    sync_warps();
-    if (!ok) break;
-    float f[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int x = 0; x < kFewWarps; ++x) top = fmaxf(top, s_ml[x * kFewRows + g + 8 * r].x);
-      f[r] = fast_exp2(m[r] - (top == -INFINITY ? 0.0f : top));
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
       if (g + 8 * r >= it.rows) continue;
+      if (c == 0) s_ml[w * kFewRows + g + 8 * r] = make_float2(m[r], l[r]);
       float* dst = s_o + (w * kFewRows + g + 8 * r) * D + 2 * c;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        *reinterpret_cast<float2*>(dst + i * 8) =
-            make_float2(o[i][2 * r] * f[r], o[i][2 * r + 1] * f[r]);
+        *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
     }
-    sync_warps();
+    warp_arrive(&bar->sync);
+    ok = mbar_wait(&bar->sync, items & 1, abort_flag, p.status);
     if (!ok) break;
     const Pieces& part = p.part[it.shared ? 0 : 1];
     const int64_t slot = static_cast<int64_t>(it.lo > 0 ? blockIdx.x : it.id) * part.stride;
@@ -1300,27 +1284,23 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
     float2* out_ml = (it.lo > 0 ? part.head_ml : part.first_ml) + slot;
     for (int i = tid; i < it.rows * (D / 4); i += kFewWarps * 32) {
       const int r = i / (D / 4), ch = i % (D / 4);
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kFewWarps; ++j) top = fmaxf(top, s_ml[j * kFewRows + r].x);
       float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int i4 = 0; i4 < kFewWarps; ++i4) {
-        const float4 y = *reinterpret_cast<const float4*>(s_o + (i4 * kFewRows + r) * D + ch * 4);
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      for (int j = 0; j < kFewWarps; ++j) {
+        const float2 ml = s_ml[j * kFewRows + r];
+        const float f = fast_exp2(ml.x - (top == -INFINITY ? 0.0f : top));
+        const float4 y = *reinterpret_cast<const float4*>(s_o + (j * kFewRows + r) * D + ch * 4);
+        x = make_float4(x.x + y.x * f, x.y + y.y * f, x.z + y.z * f, x.w + y.w * f);
+        sum += ml.y * f;
       }
       out[i] = x;
-      if (ch == 0) {
-        float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-        for (int x = 0; x < kFewWarps; ++x) top = fmaxf(top, s_ml[x * kFewRows + r].x);
-#pragma unroll
-        for (int x4 = 0; x4 < kFewWarps; ++x4)
-          sum += s_ml[x4 * kFewRows + r].y *
-                 fast_exp2(s_ml[x4 * kFewRows + r].x - (top == -INFINITY ? 0.0f : top));
-        out_ml[r] = make_float2(top, sum);
-      }
+      if (ch == 0) out_ml[r] = make_float2(top, sum);
     }
     if (tid == 0 && it.lo == 0) part.info[it.id] = make_int2(blockIdx.x, it.pieces);
-    sync_warps();  // s_o and s_ml are free again
-    if (!ok) break;
+    __syncwarp();
   }
 }
 
