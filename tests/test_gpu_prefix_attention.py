@@ -151,6 +151,9 @@ CASES = {
     "batch_1024": (1024, 1, 1, 64, 16, 33, 1, [i % 3 for i in range(1024)]),
     "one_sequence": (1, 8, 2, 128, 64, 1000, 5, [5]),
     "heads_40": (2, 40, 40, 64, 16, 90, 1, [3, 20]),
+    # warps without rows beside warps with them, over many blocks
+    "second_tile_of_few_rows": (36, 8, 2, 64, 32, 5000, 1, [i % 50 for i in range(36)]),
+    "one_tile_of_some_rows": (60, 16, 16, 64, 128, 300, 1, [900 + 7 * i for i in range(60)]),
     # several long items to every CTA
     "long_tails_of_many": (12, 24, 24, 64, 64, 300, 1, [900 + 97 * i for i in range(12)]),
     "long_tails_of_rows": (12, 24, 12, 128, 128, 700, 20, [600 + 97 * i for i in range(12)]),
@@ -206,10 +209,11 @@ def test_a_sequence_shorter_than_the_prefix_sees_the_prefix_alone(svg):
 
 
 def test_equal_results_on_every_call(svg):
-    for name in ("grouped", "one_row_long", "rows_700"):
+    for name in ("grouped", "one_row_long", "rows_700", "second_tile_of_few_rows",
+                 "one_tile_of_some_rows", "rows_129"):
         c = Case(svg, *CASES[name], seed=11).call(svg)
         o, lse = c.o.clone(), c.lse.clone()
-        for _ in range(5):
+        for _ in range(20):
             c.o.fill_(1.0)
             svg.svg_prefix_attention(*c.args, c.ws)
             assert torch.equal(c.o, o) and torch.equal(c.lse, lse)

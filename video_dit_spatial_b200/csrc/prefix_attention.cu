@@ -437,15 +437,35 @@ __device__ __forceinline__ void stream_blocks(const Params& p, const CUtensorMap
   const bool loads = pn < kPanels;
   const int past = p.c.n_pages * p.c.H_kv * p.c.ps;
   Order it = {};
+  // 64 consecutive page numbers of a sequence, lane i the i-th of either half; the second
+  // half is on its way while the first is used, so that only an item's first block waits
+  // for the table (a load of it takes as long as a block's share of HBM).
+  int w_seq = -1, w_base = 0, w0 = 0, w1 = 0;
+  auto page_at = [&](int seq, int i) {
+    return i < p.c.max_pages ? __ldg(p.table + static_cast<int64_t>(seq) * p.c.max_pages + i) : -1;
+  };
   // row of the pool that this lane's box of block k begins at
   auto row_of = [&](int k) {
     const bool own = k >= it.pre;
     const int lo = k == it.pre ? it.lo_own : 0;
     const int hi = k == it.pre - 1 ? it.hi_pre : own && k == it.nb - 1 ? it.hi_last : BK;
+    const int seq = own ? it.seq : p.prefix_seq;
+    const int pos0 = (own ? k - it.pre + it.blk0 : k) * BK;
+    const int first = pos0 / p.c.ps, pos = pos0 + bx * box;
+    if (seq != w_seq || first < w_base || first >= w_base + 64) {
+      w_seq = seq;
+      w_base = first;
+      w0 = page_at(seq, first + lane);
+      w1 = page_at(seq, first + 32 + lane);
+    } else if (first >= w_base + 32) {
+      w_base += 32;
+      w0 = w1;
+      w1 = page_at(seq, w_base + 32 + lane);
+    }
+    const int at = loads ? pos / p.c.ps - w_base : 0;  // at most 7 past `first`
+    const int p0 = __shfl_sync(0xffffffffu, w0, at & 31), p1 = __shfl_sync(0xffffffffu, w1, at & 31);
     if (!loads || bx * box >= hi || (bx + 1) * box <= lo) return past;
-    const int pos = (own ? k - it.pre + it.blk0 : k) * BK + bx * box;
-    const int page = __ldg(p.table + static_cast<int64_t>(own ? it.seq : p.prefix_seq) * p.c.max_pages +
-                           pos / p.c.ps);
+    const int page = at < 32 ? p0 : p1;
     if (page >= 0 && page < p.c.n_pages)
       return (page * p.c.H_kv + it.kv) * p.c.ps + pos % p.c.ps;
     atomicOr(p.status, kDevErrBounds);
@@ -454,10 +474,8 @@ __device__ __forceinline__ void stream_blocks(const Params& p, const CUtensorMap
   int n = 0;  // blocks issued
   bool ok = true;
   while (ok && orders.take(it)) {
-    int y = row_of(it.lo);
     for (int k = it.lo; k < it.hi; ++k, ++n) {
-      const int y0 = y;
-      if (k + 1 < it.hi) y = row_of(k + 1);  // the next block's page, while this one waits
+      const int y = row_of(k);
       const int st = n % STAGES;
       if (lane == 0) {
         ok = mbar_wait(&empty[st], ((n / STAGES) & 1) ^ 1, orders.abort_flag, p.status);
@@ -466,7 +484,7 @@ __device__ __forceinline__ void stream_blocks(const Params& p, const CUtensorMap
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       if (loads)
-        tma_load_3d(ring + st * kTile + pn * kPanel + bx * box * 128, map, &full[st], pn * 64, y0, 0);
+        tma_load_3d(ring + st * kTile + pn * kPanel + bx * box * 128, map, &full[st], pn * 64, y, 0);
     }
   }
   if (*orders.abort_flag && lane == 0) {
@@ -827,8 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float m_new = rebase ? m_tile : m;
           const float alpha = rebase ? fast_exp2(m - m_new) : 1.0f;
           const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+          // P and O are free again once the previous block's product is done
           if (C::kOwnP && sc > 0) {
-            // P and O are free again: the previous block's product is done
             ok = mbar_wait(&bar->pv_done[t], (sc - 1) & 1, abort_flag, p.status);
             __syncwarp();
             tc_fence_after();
@@ -867,6 +885,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_wait();
           }
         }
+        // A warp without rows waits for that product too: its arrival for this block
+        // must not be taken for one for the previous block, whose P may still be on its way.
+        if (C::kOwnP && !active && sc > 0)
+          ok = mbar_wait(&bar->pv_done[t], (sc - 1) & 1, abort_flag, p.status);
         // Values that do not count may hold anything; a weight of 0 times NaN is
         // NaN, so their rows are cleared before the product reads them (by
         // both tiles' threads: either product may come first).
@@ -1333,10 +1355,12 @@ __device__ __forceinline__ void store_row(const Params& p, int64_t row, int c4, 
     p.lse[row] = s.l > 0.0f ? (s.m + __log2f(s.l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// Pieces k = first, first + step, ... of row r of an item.
+// Pieces k = first, first + step, ... of row r of an item. (A count that cannot be, where a
+// kernel gave up before it wrote one, is not followed.)
 template <int D>
 __device__ __forceinline__ void join_pieces(Joined& s, const Pieces& part, int2 info,
                                             int64_t first_slot, int r, int c4, int first, int step) {
+  if (info.x < 0 || info.y < 0 || info.x > kMaxCtas || info.y > kMaxCtas - info.x) return;
 #pragma unroll 8
   for (int k = first; k < info.y; k += step) {
     const int64_t slot = (k == 0 ? first_slot : info.x + k) * part.stride;
