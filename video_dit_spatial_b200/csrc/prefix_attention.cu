@@ -176,7 +176,7 @@ struct Cfg {
   static constexpr int kOffBar = kOffMl + 2 * 2 * 128 * 8;
   static constexpr int kOffOrder = kOffBar + 512;
   static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);  // cum, seq, len
-  static constexpr int kUsed = kOffBatch + (kMaxBatch + 1) * 8 + 2 * kMaxBatch * 4 + 1024;
+  static constexpr int kUsed = kOffBatch + (kMaxBatch + 2) * 8 + 2 * kMaxBatch * 4 + 1024;
   static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA per SM
   static_assert(sizeof(Barriers) <= 512, "barriers");
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
@@ -198,15 +198,16 @@ struct FewCfg {
   static constexpr int kTile = D / 64 * kPanel;    // 16 KB
   static constexpr int kStages = 4;
   static constexpr int kQRow = D * 2 + 16;         // bytes from row to row: no bank conflicts
+  static constexpr int kORow = D + 8;              // floats, likewise
   static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + kStages * kTile;
-  static constexpr int kOffO = kOffV + kStages * kTile;  // float [2][warps][16][D], by turns
-  static constexpr int kOffMl = kOffO + 2 * kFewWarps * kFewRows * D * 4;
+  static constexpr int kOffO = kOffV + kStages * kTile;  // float [2][warps][16][kORow], by turns
+  static constexpr int kOffMl = kOffO + 2 * kFewWarps * kFewRows * kORow * 4;
   static constexpr int kOffQ = kOffMl + 2 * kFewWarps * kFewRows * 8;
   static constexpr int kOffBar = kOffQ + 2 * kFewRows * kQRow;
   static constexpr int kOffOrder = kOffBar + 512;
   static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);
-  static constexpr int kSmem = kOffBatch + (kMaxBatch + 1) * 8 + 2 * kMaxBatch * 4 + 1024;
+  static constexpr int kSmem = kOffBatch + (kMaxBatch + 2) * 8 + 2 * kMaxBatch * 4 + 1024;
   static_assert(sizeof(FewBarriers) <= 512, "barriers");
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -343,15 +344,16 @@ __device__ __forceinline__ bool cut_piece(int n_ctas, int64_t total, int64_t& fr
 }
 
 // SMs that the few-row kernel takes of n while the tile kernel has the rest: as the
-// cycles of their work, some 1500 for one of its blocks (an item's beginning and
-// end among them) and 1000 for a unit of the tile kernel's cost. Both kernels are
+// cycles of their work, some 1000 for one of its blocks, 2000 for an item's beginning
+// and end, and 1000 for a unit of the tile kernel's cost. Both kernels are
 // launched with n CTAs and those past their share leave at once, since the lengths
 // are not known on the host. At d = 128, one kernel after the other and side by
 // side: rows of 64 sequences over 20001 shared rows and up to 700 of their own,
-// four query heads to a key head, 79 and 71 us; of 200 over 30000 and up to 300, eight, 90 and 87 us.
-__device__ __forceinline__ int few_share(int n, int64_t few_blocks, int64_t tile_cost) {
-  if (few_blocks == 0) return 0;
-  const int64_t s = n * 3 * few_blocks / (3 * few_blocks + 2 * tile_cost);
+// four query heads to a key head, 79 and 61 us; of 40 over 20000 and 64, 24 heads, 82 and 68 us.
+__device__ __forceinline__ int few_share(int n, int64_t blocks, int64_t items, int64_t tile_cost) {
+  if (blocks == 0) return 0;
+  const int64_t few = blocks + 2 * items;
+  const int64_t s = n * few / (few + tile_cost);
   return s < 1 ? 1 : s > n - 1 ? n - 1 : static_cast<int>(s);
 }
 
@@ -377,8 +379,10 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
   __syncthreads();
   if (tid < 32) {
     int64_t sum = 0;
+    int some = 0;  // sequences with blocks
     for (int b0 = 0; b0 < z.B; b0 += 32) {
       int64_t x = b0 + tid < z.B ? s_cum[b0 + tid + 1] : 0;
+      some += __popc(__ballot_sync(0xffffffffu, x > 0));
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -388,14 +392,17 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
       if (b0 + tid < z.B) s_cum[b0 + tid + 1] = x;
       sum = __shfl_sync(0xffffffffu, x, 31);
     }
-    if (tid == 0) s_cum[0] = 0;
+    if (tid == 0) {
+      s_cum[0] = 0;
+      s_cum[z.B + 1] = some;
+    }
   }
   __syncthreads();
   const int64_t own = s_cum[z.B] * z.H_kv;  // blocks, of one group of rows each
   const int64_t shared = ok_prefix ? z.shared_cost : 0;
   int n = z.n_ctas;
   if (z.mixed) {
-    const int few = few_share(n, own, shared);
+    const int few = few_share(n, own, s_cum[z.B + 1] * z.H_kv, shared);
     n = z.own ? few : n - few;
   }
   total = (z.own ? own * z.cost_s : 0) + (z.shared ? shared : 0);
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Barriers* bar = reinterpret_cast<Barriers*>(smem + C::kOffBar);
   Order* s_order = reinterpret_cast<Order*>(smem + C::kOffOrder);
   int64_t* s_cum = reinterpret_cast<int64_t*>(smem + C::kOffBatch);
-  int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 1);
+  int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 2);
   int* s_len = s_seq + kMaxBatch;
   volatile int* abort_flag = &bar->abort_flag;
   const Sizes& z = p.z;
@@ -1072,7 +1079,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   FewBarriers* bar = reinterpret_cast<FewBarriers*>(smem + C::kOffBar);
   Order* s_order = reinterpret_cast<Order*>(smem + C::kOffOrder);
   int64_t* s_cum = reinterpret_cast<int64_t*>(smem + C::kOffBatch);
-  int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 1);
+  int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 2);
   int* s_len = s_seq + kMaxBatch;
   volatile int* abort_flag = &bar->abort_flag;
   const Sizes& z = p.z;
@@ -1182,28 +1189,33 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
       ok = mbar_wait(&bar->k_full[st], par, abort_flag, p.status);
       if (!ok) break;
       __syncwarp();
-      float s[NG][2][4], s2[NG][2][4];  // two chains of products each
+      // All of K's operands first (with one warp to a scheduler nothing else hides their
+      // latency), then the products, in two chains for each 8 keys.
+      float s[NG][2][4], s2[NG][2][4];
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < NG; ++n) {
+        uint32_t kb[D / 16][4];
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          ldmatrix4(kb[kk], k_addr + st * C::kTile + at_of(k_key + n * 16, kk * 2 + k_ch));
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][u][e] = s2[n][u][e] = 0.0f;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
+        for (int kk = 0; kk < D / 16; kk += 2)
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          uint32_t b[4];
-          ldmatrix4(b, k_addr + st * C::kTile + at_of(k_key + n * 16, kk * 2 + k_ch));
-          mma_16816((kk & 1 ? s2 : s)[n][0], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[0], b[1]);
-          mma_16816((kk & 1 ? s2 : s)[n][1], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], b[2], b[3]);
-        }
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
+          for (int u = 0; u < 2; ++u) {
+            mma_16816(s[n][u], qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3], kb[kk][2 * u],
+                      kb[kk][2 * u + 1]);
+            mma_16816(s2[n][u], qa[kk + 1][0], qa[kk + 1][1], qa[kk + 1][2], qa[kk + 1][3],
+                      kb[kk + 1][2 * u], kb[kk + 1][2 * u + 1]);
+          }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[n][u][e] += s2[n][u][e];
+      }
       warp_arrive(&bar->k_empty[st]);
       if (ragged) {
 #pragma unroll
@@ -1268,13 +1280,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
                       (key + 1 >= k_lo && key + 1 < k_hi ? 0xffff0000u : 0u);
           }
         }
+        uint32_t vb[D / 16][4];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          ldmatrix4_trans(vb[i], v_addr + st * C::kTile + at_of(v_key + n * 16, i * 2 + v_ch));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          uint32_t b[4];
-          ldmatrix4_trans(b, v_addr + st * C::kTile + at_of(v_key + n * 16, i * 2 + v_ch));
-          if (ragged) b[0] &= keep[0], b[1] &= keep[1], b[2] &= keep[0], b[3] &= keep[1];
-          mma_16816(o[2 * i], pa[n][0], pa[n][1], pa[n][2], pa[n][3], b[0], b[1]);
-          mma_16816(o[2 * i + 1], pa[n][0], pa[n][1], pa[n][2], pa[n][3], b[2], b[3]);
+          if (ragged)
+            vb[i][0] &= keep[0], vb[i][1] &= keep[1], vb[i][2] &= keep[0], vb[i][3] &= keep[1];
+          mma_16816(o[2 * i], pa[n][0], pa[n][1], pa[n][2], pa[n][3], vb[i][0], vb[i][1]);
+          mma_16816(o[2 * i + 1], pa[n][0], pa[n][1], pa[n][2], pa[n][3], vb[i][2], vb[i][3]);
         }
       }
       warp_arrive(&bar->v_empty[st]);
@@ -1284,7 +1299,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
     // ---- the four warps' (O, m, l) joined; in places by turns, so that one meeting
     // of the warps an item is enough: whoever writes a place again has met
     // the others after they read it
-    float* s_o = reinterpret_cast<float*>(smem + C::kOffO) + (items & 1) * kFewWarps * kFewRows * D;
+    float* s_o =
+        reinterpret_cast<float*>(smem + C::kOffO) + (items & 1) * kFewWarps * kFewRows * C::kORow;
     float2* s_ml = reinterpret_cast<float2*>(smem + C::kOffMl) + (items & 1) * kFewWarps * kFewRows;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -1292,7 +1308,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       if (g + 8 * r >= it.rows) continue;
       if (c == 0) s_ml[w * kFewRows + g + 8 * r] = make_float2(m[r], l[r]);
-      float* dst = s_o + (w * kFewRows + g + 8 * r) * D + 2 * c;
+      float* dst = s_o + (w * kFewRows + g + 8 * r) * C::kORow + 2 * c;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         *reinterpret_cast<float2*>(dst + i * 8) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
@@ -1314,7 +1330,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
       for (int j = 0; j < kFewWarps; ++j) {
         const float2 ml = s_ml[j * kFewRows + r];
         const float f = fast_exp2(ml.x - (top == -INFINITY ? 0.0f : top));
-        const float4 y = *reinterpret_cast<const float4*>(s_o + (j * kFewRows + r) * D + ch * 4);
+        const float4 y = *reinterpret_cast<const float4*>(s_o + (j * kFewRows + r) * C::kORow + ch * 4);
         x = make_float4(x.x + y.x * f, x.y + y.y * f, x.z + y.z * f, x.w + y.w * f);
         sum += ml.y * f;
       }
