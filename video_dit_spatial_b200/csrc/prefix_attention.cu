@@ -664,6 +664,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (orders.take(it)) {
         const int n = __shfl_sync(0xffffffffu, it.hi - it.lo, 0);
         const bool two = __shfl_sync(0xffffffffu, it.rows, 0) > 128;
+        if (!C::kOwnP && two) {
+          // P is where S was, so a tile's Q K^T follows its P V anyway: P V and Q K^T of one
+          // tile, then of the other.
+          auto wait = [&](uint64_t* b, uint32_t parity) {
+            ok = ok && mbar_wait(b, parity, abort_flag, p.status);
+            ok = __all_sync(0xffffffffu, ok) != 0;
+            return ok;
+          };
+          for (int j = 0; j <= n; ++j) {
+            const int st = (n0 + j) % C::kStages, vst = (n0 + j + C::kStages - 1) % C::kStages;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (j > 0) {
+                if (t == 0 && !wait(&bar->v_full[vst], ((n0 + j - 1) / C::kStages) & 1)) break;
+                if (t == 0 && j == 1 && items > 0 && !wait(&bar->o_free, (items - 1) & 1)) break;
+                if (!wait(&bar->p_full[t], (pp >> t) & 1u)) break;
+                pp ^= 1u << t;
+                tc_fence_after();
+                pv(t, vst, j == 1);
+                if (t == 1) tc_commit_on(on, &bar->v_empty[vst]);
+                if (j == n) tc_commit_on(on, &bar->o_final[t]);
+              }
+              if (j < n) {
+                if (j == 0 && !wait(&bar->q_full[(qn + t) & 1], ((qn + t) >> 1) & 1)) break;
+                if (t == 0 && !wait(&bar->k_full[st], ((n0 + j) / C::kStages) & 1)) break;
+                tc_fence_after();
+                qk(t, (qn + t) & 1, st);
+                if (t == 1) tc_commit_on(on, &bar->k_empty[st]);
+                if (j == n - 1) tc_commit_on(on, &bar->q_empty[(qn + t) & 1]);
+              }
+            }
+            if (!ok) break;
+          }
+          if (!ok) break;
+          n0 += n;
+          qn += 2;
+          ++items;
+          continue;
+        }
         // The products that may come next (two tiles, Q K^T or P V) are issued as
         // their operands get ready; in a fixed order one tile waits for what
         // the other's softmax has still to do. With one tile of rows tile 1 has the odd
