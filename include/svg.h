@@ -584,7 +584,8 @@ svg_status svg_cache_copy_pages(const svg_cache_geom* geom, const int32_t* moves
                                 svg_bf16* k_dst, svg_bf16* v_dst, svg_stream_t stream);
 
 /* svg_prefix_attention_workspace_bytes -- host only: device workspace
- * svg_prefix_attention needs for B entries of Lq query rows and H heads. */
+ * svg_prefix_attention needs for B entries of Lq query rows and H heads. It
+ * does not fall with B or Lq: a workspace for the largest call serves all. */
 svg_status svg_prefix_attention_workspace_bytes(const svg_cache_geom* geom, int32_t B, int32_t H,
                                                 int32_t Lq, size_t* bytes);
 

@@ -101,6 +101,19 @@ def test_list_lengths_and_shapes_are_refused(svg):
         svg.svg_prefix_attention_workspace_bytes(g, 2, 3, 3)
 
 
+@pytest.mark.parametrize("H,H_kv,d", [(8, 8, 64), (8, 2, 128), (64, 1, 128), (40, 1, 64)])
+def test_a_workspace_for_the_largest_call_serves_the_smaller_ones(svg, H, H_kv, d):
+    g = _geom(svg, n_pages=1000, H_kv=H_kv, d=d)
+    rows = [1, 2, 3, 4, 7, 16, 17, 31, 40, 64, 129, 200, 256, 257, 400, 513, 900, 2304, 2305, 5000]
+    most = {}
+    for B in (1, 2, 3, 5, 8, 17, 40, 300, 1024):
+        before = 0
+        for L in rows:
+            n = svg.svg_prefix_attention_workspace_bytes(g, B, H, L)
+            assert n >= before and n >= most.get(L, 0)
+            most[L] = before = n
+
+
 def test_binding_refuses_host_tensors(svg):
     import torch
     g = _geom(svg)

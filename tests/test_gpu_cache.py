@@ -168,6 +168,25 @@ def test_no_room_leaves_everything(svg):
     b.check()
 
 
+def test_more_pages_wanted_than_an_int_counts(svg):
+    """1024 entries that want 2^22 + 1 pages each, 2^32 + 1024 between them: nothing is reserved."""
+    width = (1 << 22) + 1
+    geom = svg.CacheGeom(64, 256, 1, 64, 1025, 1 << 20)
+    small = svg.CacheGeom(64, 16, 1, 64, 505, width)  # 505 * width entries fit 2^31
+    for g, counts in ((geom, (1 << 20) * 256), (small, 16 * width)):
+        n = min(1024, g.max_seqs)
+        table = torch.full((g.max_seqs, g.max_pages), -1, dtype=torch.int32, device="cuda")
+        lens = torch.zeros(g.max_seqs, dtype=torch.int32, device="cuda")
+        refs = torch.zeros(64, dtype=torch.int32, device="cuda")
+        plan = torch.zeros((n, 4), dtype=torch.int32, device="cuda")
+        seqs = torch.arange(n, dtype=torch.int32, device="cuda")
+        svg.svg_cache_reserve(g, table, lens, refs, seqs, torch.full_like(seqs, counts), plan)
+        assert svg.svg_get_device_status()[1] == 4
+        assert not lens.any() and not refs.any() and torch.all(table == -1)
+        assert torch.all(plan[:, 1] == 0) and torch.all(plan[:, 2:] == -1)
+        del table
+
+
 def test_refused_entries_change_nothing(svg):
     b = Both(svg, 20, 16, 1, 64, 5, 3)
     b.append([0, 1], [20, 5])

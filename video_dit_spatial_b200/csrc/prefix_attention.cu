@@ -1540,7 +1540,7 @@ Layout layout(const CacheDims& c, int32_t B, int32_t H, int32_t Lq, Form form) {
   };
   l.head_item = take(kMaxCtas * sizeof(int32_t));
   for (int i = 0; i < 2; ++i) {
-    if (form == kJoint && i == 0) continue;
+    if (i == 0 && (form == kJoint || (form == kFew && B * GL > kFewRows))) continue;  // no shared items
     Place& t = l.part[i];
     const bool few = form == kFew || (form == kMixed && i == 1);
     const int all = i == 0 ? B * GL : GL;
@@ -1662,11 +1662,27 @@ cudaError_t launch(const PrefixArgs& a, Params& p, Form form, int sms, cudaStrea
 
 }  // namespace
 
+// What the call itself needs, and what calls of fewer entries or rows might, which another
+// form may take: above 2304 rows a sequence the groups are at least nine tenths
+// full, so that all calls are joint.
 size_t prefix_workspace_bytes(const CacheDims& c, int32_t B, int32_t H, int32_t Lq) {
-  const int GL = H / c.H_kv * Lq;
-  const size_t with = layout(c, B, H, Lq, form_of(B, GL, true)).bytes;
-  const size_t without = layout(c, B, H, Lq, form_of(B, GL, false)).bytes;
-  return with > without ? with : without;
+  const int G = H / c.H_kv, GL = G * Lq;
+  size_t most = 0;
+  auto take = [&](Form form, int32_t rows) {
+    const size_t n = layout(c, B, H, rows, form).bytes;
+    if (n > most) most = n;
+  };
+  if (GL <= kFewRows) {
+    take(kFew, Lq);
+    take(kMixed, Lq);
+  } else {
+    take(kJoint, Lq);
+    const int rows = 2304 / G < 1 ? 1 : 2304 / G;  // of more heads to a key head one row is more
+    take(kGathered, Lq < rows ? Lq : rows);
+  }
+  take(form_of(B, GL, true), Lq);
+  take(form_of(B, GL, false), Lq);
+  return most;
 }
 
 cudaError_t launch_prefix_attention(const PrefixArgs& a, int* status, cudaStream_t stream) {
