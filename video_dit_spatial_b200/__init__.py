@@ -378,17 +378,18 @@ def svg2_sparse_attention(BH, N, d, block_k, scale, qs, ks, vs, row_ptr, col_idx
 # history cache and the attention that reads it
 # ---------------------------------------------------------------------------
 _torch = None
+_has_device = False
 
 
 def _here():
     """torch and the current device's index, for the checks below."""
-    global _torch
+    global _torch, _has_device
     if _torch is None:
         import torch
+        _has_device = torch.cuda.is_available()
         _torch = torch
-    if not _torch.cuda.is_initialized() and not _torch.cuda.is_available():
-        return _torch, -2  # no device: no tensor passes the checks
-    return _torch, _torch.cuda.current_device()
+    # without a device no tensor passes the checks
+    return _torch, _torch.cuda.current_device() if _has_device else -2
 
 
 def _buf(name: str, x, dtype, numel: int, dev: int) -> Optional[int]:
@@ -421,9 +422,8 @@ def _state(geom: CacheGeom, table, lens, refs, i32, dev: int):
             _buf("refs", refs, i32, geom.n_pages, dev))
 
 
-def _pool(geom: CacheGeom, bf16, dev: int, **pages):
-    n = geom.n_pages * geom.H_kv * geom.page_size * geom.head_dim
-    return [_buf(name, x, bf16, n, dev) for name, x in pages.items()]
+def _pool_values(geom: CacheGeom) -> int:
+    return geom.n_pages * geom.H_kv * geom.page_size * geom.head_dim
 
 
 def svg_cache_reset(geom: CacheGeom, table, lens, refs, stream=None) -> None:
@@ -469,12 +469,13 @@ def svg_cache_write(geom: CacheGeom, table, seqs, plan, L, k_new, v_new, k_pages
     torch, dev = _here()
     i32, bf16 = torch.int32, torch.bfloat16
     n = seqs.numel() if n is None else n
-    rows = n * geom.H_kv * L * geom.head_dim
+    rows, values = n * geom.H_kv * L * geom.head_dim, _pool_values(geom)
     _check("svg_cache_write", load().svg_cache_write(
         ctypes.byref(geom), _buf("table", table, i32, geom.max_seqs * geom.max_pages, dev),
         _buf("seqs", seqs, i32, n, dev), _buf("plan", plan, i32, 4 * n, dev), n, L,
         _buf("k_new", k_new, bf16, rows, dev), _buf("v_new", v_new, bf16, rows, dev),
-        *_pool(geom, bf16, dev, k_pages=k_pages, v_pages=v_pages), _stream_on(dev, stream)))
+        _buf("k_pages", k_pages, bf16, values, dev), _buf("v_pages", v_pages, bf16, values, dev),
+        _stream_on(dev, stream)))
 
 
 def svg_cache_compact(geom: CacheGeom, table, refs, table_out, refs_out, moves,
@@ -492,9 +493,11 @@ def svg_cache_compact(geom: CacheGeom, table, refs, table_out, refs_out, moves,
 def svg_cache_copy_pages(geom: CacheGeom, moves, max_moves, k_src, v_src, k_dst, v_dst,
                          stream=None) -> None:
     torch, dev = _here()
+    bf16, values = torch.bfloat16, _pool_values(geom)
     _check("svg_cache_copy_pages", load().svg_cache_copy_pages(
         ctypes.byref(geom), _buf("moves", moves, torch.int32, 2 + 2 * max_moves, dev), max_moves,
-        *_pool(geom, torch.bfloat16, dev, k_src=k_src, v_src=v_src, k_dst=k_dst, v_dst=v_dst),
+        _buf("k_src", k_src, bf16, values, dev), _buf("v_src", v_src, bf16, values, dev),
+        _buf("k_dst", k_dst, bf16, values, dev), _buf("v_dst", v_dst, bf16, values, dev),
         _stream_on(dev, stream)))
 
 
@@ -509,14 +512,14 @@ def svg_prefix_attention(geom: CacheGeom, B, H, Lq, prefix_seq, prefix_len, scal
                          v_pages, table, lens, seqs, o, lse, workspace, workspace_bytes=None,
                          stream=None) -> None:
     torch, dev = _here()
-    i32, bf16, rows = torch.int32, torch.bfloat16, B * H * Lq
+    i32, bf16, rows, values = torch.int32, torch.bfloat16, B * H * Lq, _pool_values(geom)
     wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
     ws = _buf("workspace", workspace, workspace.dtype, 0, dev) \
         if workspace.__class__ is not int else workspace
     _check("svg_prefix_attention", load().svg_prefix_attention(
         ctypes.byref(geom), B, H, Lq, prefix_seq, prefix_len, scale,
         _buf("q", q, bf16, rows * geom.head_dim, dev),
-        *_pool(geom, bf16, dev, k_pages=k_pages, v_pages=v_pages),
+        _buf("k_pages", k_pages, bf16, values, dev), _buf("v_pages", v_pages, bf16, values, dev),
         _buf("table", table, i32, geom.max_seqs * geom.max_pages, dev),
         _buf("lens", lens, i32, geom.max_seqs, dev), _buf("seqs", seqs, i32, B, dev),
         _buf("o", o, bf16, rows * geom.head_dim, dev), _buf("lse", lse, torch.float32, rows, dev),
