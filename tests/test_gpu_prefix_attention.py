@@ -165,6 +165,24 @@ def test_parity(svg, name):
     Case(svg, *CASES[name], seed=sorted(CASES).index(name)).call(svg).compare(name)
 
 
+# More items than SMs, so that each SM has whole ones before its piece of the rest: of one
+# sequence each, with a prefix and without, of all sequences together, and beside the
+# kernel for few rows. Some sequences have no rows of their own.
+DEALT = {
+    "own_and_prefix": (3, 40, 40, 64, 64, 600, 900, [900, 0, 1400]),
+    "own": (6, 24, 24, 128, 16, 0, 260, [700, 690, 0, 701, 640, 768]),
+    "gathered": (30, 60, 60, 64, 32, 700, 20, [7 * b for b in range(30)]),
+    "gathered_long": (5, 80, 80, 128, 128, 2000, 60, [60, 0, 200, 61, 1000]),
+    "beside_few_rows": (150, 240, 60, 64, 16, 1000, 1, [b % 60 for b in range(150)]),
+}
+
+
+@pytest.mark.parametrize("name", sorted(DEALT))
+@pytest.mark.parametrize("idle", [(), (1,)])
+def test_more_items_than_sms(svg, name, idle):
+    Case(svg, *DEALT[name], seed=17, idle=idle).call(svg).compare(name)
+
+
 @pytest.mark.parametrize("name", ["grouped", "tiles_cross_sequences", "rows_257"])
 def test_idle_entries_keep_their_rows(svg, name):
     a = CASES[name]

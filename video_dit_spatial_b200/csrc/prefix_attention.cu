@@ -18,7 +18,8 @@
 // equal piece per CTA: every SM gets the same work whatever the lengths
 // are, which only the device knows. A piece begins and ends anywhere in an
 // item; what a CTA has of an item that is not whole is written as (O, m, l) in
-// fp32 and joined by a second kernel.
+// fp32 and joined by a second kernel. Where there are several items to a CTA, whole
+// ones are dealt out first and only the rest is cut (see Cuts).
 //
 // One CTA per SM walks its piece. 384 threads: warps 0-3 and 4-7 softmax
 // and epilogue (thread = row = tensor-memory lane), warp 8 loads K, warp 9 issues
@@ -54,6 +55,7 @@ constexpr int kBK = 128;             // keys of a block
 constexpr int kGroup = 256;          // rows of an item
 constexpr int kMaxCtas = 148;
 constexpr int kMaxBatch = 1024;
+constexpr int kMaxRounds = 16;       // in which items are dealt out
 constexpr int kFewRows = 16;    // rows of an item of the few-row kernel
 constexpr int kFewWarps = 4;    // that compute
 // Cost of a block: a two-tile block keeps the tensor core and the exponentials
@@ -175,8 +177,9 @@ struct Cfg {
   static constexpr int kOffMl = kOffV + kStages * kTile;          // float2 [2][2][128]
   static constexpr int kOffBar = kOffMl + 2 * 2 * 128 * 8;
   static constexpr int kOffOrder = kOffBar + 512;
-  static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);  // cum, seq, len
-  static constexpr int kUsed = kOffBatch + (kMaxBatch + 2) * 8 + 2 * kMaxBatch * 4 + 1024;
+  static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);  // cum, cuts, rounds, seq, len
+  static constexpr int kUsed = kOffBatch + (kMaxBatch + 4 + kMaxCtas + 2 + 2 * (kMaxRounds + 1)) * 8 +
+                               2 * kMaxBatch * 4 + 1024;
   static constexpr int kSmem = kUsed > 120 * 1024 ? kUsed : 120 * 1024;  // one CTA per SM
   static_assert(sizeof(Barriers) <= 512, "barriers");
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
@@ -207,7 +210,7 @@ struct FewCfg {
   static constexpr int kOffBar = kOffQ + 2 * kFewRows * kQRow;
   static constexpr int kOffOrder = kOffBar + 512;
   static constexpr int kOffBatch = kOffOrder + kOrders * sizeof(Order);
-  static constexpr int kSmem = kOffBatch + (kMaxBatch + 2) * 8 + 2 * kMaxBatch * 4 + 1024;
+  static constexpr int kSmem = kOffBatch + (kMaxBatch + 3) * 8 + 2 * kMaxBatch * 4 + 1024;
   static_assert(sizeof(FewBarriers) <= 512, "barriers");
   static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
 };
@@ -245,11 +248,14 @@ struct Walk {
   int64_t at, from, to;  // cost at which the current item begins
   int shared, kv, b, g;
 
+  __host__ __device__ Walk(const Sizes& sizes, const int64_t* cum_) : z(sizes), cum(cum_) {}
+
   __host__ __device__ __forceinline__ int64_t own_cost() const {
     return z.own ? cum[z.B] * z.cost_s : 0;
   }
-  __host__ __device__ Walk(const Sizes& sizes, const int64_t* cum_, int64_t from_, int64_t to_)
-      : z(sizes), cum(cum_), from(from_), to(to_) {
+  __host__ __device__ void start(int64_t from_, int64_t to_) {
+    from = from_;
+    to = to_;
     const int64_t per = static_cast<int64_t>(z.nbp) * z.cost_p;
     const int64_t all = z.shared ? per * z.H_kv : 0;
     int64_t rest = from;
@@ -330,17 +336,50 @@ __device__ __forceinline__ int64_t q_row(const Sizes& z, const Item& it, int r) 
   return (static_cast<int64_t>(b) * z.H_kv + it.kv) * z.GL + r;
 }
 
+// Cost at which item i begins, in the order of the walk (those without blocks counted).
+__host__ __device__ inline int64_t item_begin(const Sizes& z, const int64_t* cum, int64_t i) {
+  const int64_t per = z.shared ? static_cast<int64_t>(z.nbp) * z.cost_p : 0;
+  const int shared = z.shared ? z.H_kv * z.groups_p : 0;
+  if (i < shared) {
+    const int kv = static_cast<int>(i) / z.groups_p, g = static_cast<int>(i) - kv * z.groups_p;
+    return kv * per + static_cast<int64_t>(g) * z.nbp * kCostTwo;
+  }
+  const int j = static_cast<int>(i - shared), pair = j / z.groups_s, g = j - pair * z.groups_s;
+  const int kv = pair / z.B, b = pair - kv * z.B;
+  return per * z.H_kv + (kv * cum[z.B] + cum[b]) * z.cost_s +
+         g * (cum[b + 1] - cum[b]) * kCostTwo;
+}
+
+// How the line is cut. First `rounds` times n_pieces items are dealt out whole, one in
+// turn to each CTA, so that at any time the CTAs are at neighbouring items, which read the
+// same keys, and those come from L2. The rest is cut so that all CTAs have the same in all.
 // No piece is smaller than a block, so that every CTA from an item's first to
-// its last has a piece of it.
-__device__ __forceinline__ bool cut_piece(int n_ctas, int64_t total, int64_t& from, int64_t& to,
-                                          int& n_pieces) {
-  const int64_t most = total / kCostTwo < 1 ? 1 : total / kCostTwo;
-  n_pieces = static_cast<int>(most < n_ctas ? most : n_ctas);
-  const int cta = blockIdx.x;
-  if (cta >= n_pieces || total == 0) return false;
-  from = total * cta / n_pieces;
-  to = total * (cta + 1) / n_pieces;
-  return true;
+// its last has a piece of it. 3600 rows of two sequences over 7200 and 3600 rows, 24
+// heads, d = 128: one cut line reads 3.2 GB from HBM (L2 gives 35 %) and takes 1075 us, with
+// 4 rounds dealt 0.23 GB (89 %) and 929 us, most of it for the clock, which the
+// power of those reads held down. At kMaxRounds the items are so short that what all CTAs
+// have of the line at a time stays in L2 anyway.
+struct Cuts {
+  int64_t total;
+  int n_pieces, rounds;
+  const int64_t* at;  // [n_pieces + 1] where the pieces of the rest begin, with rounds
+  __host__ __device__ __forceinline__ int64_t begin(int w) const {
+    return rounds ? at[w] : total * w / n_pieces;
+  }
+};
+// Rounds of a line whose largest item costs `most`: each CTA has a block left at least.
+__host__ __device__ inline int deal_rounds(int64_t total, int n, int64_t most) {
+  const int64_t r = (total / n - kCostTwo) / most;
+  return r < 0 ? 0 : r > kMaxRounds ? kMaxRounds : static_cast<int>(r);
+}
+__host__ __device__ inline int64_t rest_begin(const Sizes& z, const int64_t* cum, const Cuts& c, int w) {
+  int64_t before = 0;  // cost dealt to the CTAs before this one
+  for (int j = 0; j < c.rounds; ++j) {
+    const int64_t i = static_cast<int64_t>(j) * c.n_pieces;
+    before += item_begin(z, cum, i + w) - item_begin(z, cum, i);
+  }
+  return item_begin(z, cum, static_cast<int64_t>(c.rounds) * c.n_pieces) + c.total * w / c.n_pieces -
+         before;
 }
 
 // SMs that the few-row kernel takes of n while the tile kernel has the rest: as the
@@ -357,12 +396,12 @@ __device__ __forceinline__ int few_share(int n, int64_t blocks, int64_t items, i
   return s < 1 ? 1 : s > n - 1 ? n - 1 : static_cast<int>(s);
 }
 
-// The batch's lengths into shared memory and this CTA's piece [from, to) of the
-// line of cost; false: it has none. Every CTA finds the same line.
-template <int T, int BK, int FEW_BK>
-__device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int* s_seq, int* s_len,
-                                           int64_t& from, int64_t& to, int64_t& total,
-                                           int& n_pieces) {
+// The batch's lengths into shared memory and the cuts of the line of cost; false: this CTA
+// has no piece. Every CTA finds the same line. `s_at`: room for the cuts of a line
+// that is dealt.
+template <int T, int BK, int FEW_BK, bool DEAL>
+__device__ __forceinline__ bool plan_pieces(const Params& p, int64_t* s_cum, int* s_seq, int* s_len,
+                                            int64_t* s_at, Cuts& cuts) {
   const Sizes& z = p.z;
   const int tid = threadIdx.x, cta = blockIdx.x;
   const bool ok_prefix = prefix_ok(p.c, p.lens, p.prefix_seq, z.prefix_len);
@@ -380,9 +419,11 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
   if (tid < 32) {
     int64_t sum = 0;
     int some = 0;  // sequences with blocks
+    int most = 0;  // blocks of one
     for (int b0 = 0; b0 < z.B; b0 += 32) {
       int64_t x = b0 + tid < z.B ? s_cum[b0 + tid + 1] : 0;
       some += __popc(__ballot_sync(0xffffffffu, x > 0));
+      most = max(most, static_cast<int>(x));
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
@@ -392,9 +433,11 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
       if (b0 + tid < z.B) s_cum[b0 + tid + 1] = x;
       sum = __shfl_sync(0xffffffffu, x, 31);
     }
+    if (DEAL) most = __reduce_max_sync(0xffffffffu, most);
     if (tid == 0) {
       s_cum[0] = 0;
       s_cum[z.B + 1] = some;
+      if (DEAL) s_cum[z.B + 2] = most;
     }
   }
   __syncthreads();
@@ -405,17 +448,38 @@ __device__ __forceinline__ bool plan_piece(const Params& p, int64_t* s_cum, int*
     const int few = few_share(n, own, s_cum[z.B + 1] * z.H_kv, shared);
     n = z.own ? few : n - few;
   }
-  total = (z.own ? own * z.cost_s : 0) + (z.shared ? shared : 0);
-  return cut_piece(n, total, from, to, n_pieces);
+  cuts.total = (z.own ? own * z.cost_s : 0) + (z.shared ? shared : 0);
+  if (cuts.total == 0) return false;
+  const int64_t blocks = cuts.total / kCostTwo < 1 ? 1 : cuts.total / kCostTwo;
+  cuts.n_pieces = blocks < n ? static_cast<int>(blocks) : n;
+  cuts.rounds = 0;
+  cuts.at = s_at;
+  if (DEAL) {
+    const int64_t most_own = z.own ? s_cum[z.B + 2] : 0;
+    const int64_t most = z.shared && shared > 0 && z.nbp > most_own ? z.nbp : most_own;
+    cuts.rounds = deal_rounds(cuts.total, n, most * kCostTwo);
+    if (cuts.rounds > 0) {
+      for (int w = tid; w <= cuts.n_pieces; w += T) s_at[w] = rest_begin(z, s_cum, cuts, w);
+      __syncthreads();
+    }
+  }
+  return cta < cuts.n_pieces;
 }
 
-// First CTA (this one) and number of pieces of the item whose first block it has.
-__device__ __forceinline__ int2 pieces_of(const Item& it, int64_t end, int64_t total, int n_pieces) {
-  const int w = cost_of(it.rows);
-  const int64_t x = end - w;  // where the last block begins
-  int64_t last = x * n_pieces / total;
-  while (total * (last + 1) / n_pieces <= x) ++last;
-  return make_int2(blockIdx.x, static_cast<int>(last) - static_cast<int>(blockIdx.x) + 1);
+// Number of pieces of the item whose first block CTA `cta` has; it ends at `end`.
+__host__ __device__ inline int pieces_of(const Item& it, int64_t end, const Cuts& cuts, int cta) {
+  const int64_t x = end - cost_of(it.rows);  // where the last block begins
+  int last = cuts.rounds ? cta : static_cast<int>(x * cuts.n_pieces / cuts.total);
+  while (cuts.begin(last + 1) <= x) ++last;
+  return last - cta + 1;
+}
+
+// The costs between which round `j` of CTA `cta` lies; the last one is its piece of the rest.
+__host__ __device__ inline longlong2 round_range(const Sizes& z, const int64_t* cum, const Cuts& cuts,
+                                                 int cta, int j) {
+  if (j == cuts.rounds) return make_longlong2(cuts.begin(cta), cuts.begin(cta + 1));
+  const int64_t i = static_cast<int64_t>(j) * cuts.n_pieces + cta;
+  return make_longlong2(item_begin(z, cum, i), item_begin(z, cum, i + 1));
 }
 
 // One arrival for a warp's 32: arrivals on one address are taken one by one.
@@ -509,8 +573,7 @@ __device__ __forceinline__ void stream_blocks(const Params& p, const CUtensorMap
 // them. False: a wait ran out.
 template <int BK>
 __device__ __forceinline__ bool publish(const Params& p, Orders& orders, bool more, const Item& item,
-                                        const Walk& walk, int64_t total, int n_pieces,
-                                        const int* s_seq, const int* s_len) {
+                                        int pieces, const int* s_seq, const int* s_len) {
   const Sizes& z = p.z;
   const int at = orders.n % kOrders;
   const bool ok = mbar_wait(&orders.empty[at], ((orders.n / kOrders) & 1) ^ 1, orders.abort_flag,
@@ -536,7 +599,7 @@ __device__ __forceinline__ bool publish(const Params& p, Orders& orders, bool mo
         w.row0 = static_cast<int>(q_row(z, item, 0));
       }
       w.id = item.id;
-      if (item.lo == 0) w.pieces = pieces_of(item, walk.at, total, n_pieces).y;
+      w.pieces = pieces;
     }
     orders.ring[at] = w;
     mbar_arrive(&orders.full[at]);
@@ -545,7 +608,9 @@ __device__ __forceinline__ bool publish(const Params& p, Orders& orders, bool mo
   return true;
 }
 
-template <int D>
+// DEAL: there are more items than CTAs, so that some may be dealt out whole. A kernel of its
+// own, since with that code in it the others took 1.5 us longer to get going.
+template <int D, bool DEAL>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_attention_kernel(const __grid_constant__ Params p) {
   using C = Cfg<D>;
@@ -559,7 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Barriers* bar = reinterpret_cast<Barriers*>(smem + C::kOffBar);
   Order* s_order = reinterpret_cast<Order*>(smem + C::kOffOrder);
   int64_t* s_cum = reinterpret_cast<int64_t*>(smem + C::kOffBatch);
-  int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 2);
+  int64_t* s_at = s_cum + kMaxBatch + 4;
+  longlong2* s_range = reinterpret_cast<longlong2*>(s_at + kMaxCtas + 2);
+  int* s_seq = reinterpret_cast<int*>(s_range + kMaxRounds + 1);
   int* s_len = s_seq + kMaxBatch;
   volatile int* abort_flag = &bar->abort_flag;
   const Sizes& z = p.z;
@@ -572,13 +639,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&p.tm_q);
   }
 
-  int64_t from, to, total;
-  int n_pieces;
-  if (!plan_piece<kThreads, kBK, FewCfg<D>::kBlock>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) {
+  Cuts cuts;
+  if (!plan_pieces<kThreads, kBK, FewCfg<D>::kBlock, DEAL>(p, s_cum, s_seq, s_len, s_at, cuts)) {
     if (z.joint && tid == 0) p.head_item[cta] = -1;
     if (tid == 0) wait_for_primary();
     return;
   }
+  if (DEAL && tid <= cuts.rounds) s_range[tid] = round_range(z, s_cum, cuts, cta, tid);
 
   // ---- barriers and tensor memory
   if (warp == 0) {
@@ -775,11 +842,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int vec = lane % kVecs;
       int qn = 0;
       bool ok = true;
-      Walk walk(z, s_cum, from, to);
+      Walk walk(z, s_cum);
       Item item;
+      int round = DEAL ? -1 : 0;
+      if constexpr (!DEAL) walk.start(cuts.begin(cta), cuts.begin(cta + 1));
       for (bool more = true; more;) {
-        more = walk.next(item);
-        if (!publish<kBK>(p, orders, more, item, walk, total, n_pieces, s_seq, s_len)) break;
+        if constexpr (DEAL) {
+          while (round < 0 || !walk.next(item)) {
+            more = ++round <= cuts.rounds;
+            if (!more) break;
+            walk.start(s_range[round].x, s_range[round].y);
+          }
+        } else {
+          more = walk.next(item);
+        }
+        const int pieces = !more || item.lo > 0 ? 0
+                           : round < cuts.rounds ? 1 : pieces_of(item, walk.at, cuts, cta);
+        if (!publish<kBK>(p, orders, more, item, pieces, s_seq, s_len)) break;
         if (!more) break;
         for (int r0 = 0; r0 < item.rows; r0 += 128, ++qn) {
           uint64_t* full = &bar->q_full[qn & 1];
@@ -1118,7 +1197,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   FewBarriers* bar = reinterpret_cast<FewBarriers*>(smem + C::kOffBar);
   Order* s_order = reinterpret_cast<Order*>(smem + C::kOffOrder);
   int64_t* s_cum = reinterpret_cast<int64_t*>(smem + C::kOffBatch);
-  int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 2);
+  int* s_seq = reinterpret_cast<int*>(s_cum + kMaxBatch + 3);
   int* s_len = s_seq + kMaxBatch;
   volatile int* abort_flag = &bar->abort_flag;
   const Sizes& z = p.z;
@@ -1145,9 +1224,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
     bar->abort_flag = 0;
     fence_mbar_init();
   }
-  int64_t from, to, total;
-  int n_pieces;
-  if (!plan_piece<kFewThreads, C::kBlock, C::kBlock>(p, s_cum, s_seq, s_len, from, to, total, n_pieces)) return;
+  Cuts cuts;
+  if (!plan_pieces<kFewThreads, C::kBlock, C::kBlock, false>(p, s_cum, s_seq, s_len, nullptr, cuts)) return;
   __syncthreads();
   Orders orders{s_order, bar->item_full, bar->item_empty, abort_flag, p.status};
 
@@ -1161,12 +1239,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) prefix_few_kernel(const __grid
   }
   if (warp == kFewWarps + 2) {
     // ------------------------------------------------------------ orders and query rows
-    Walk walk(z, s_cum, from, to);
+    Walk walk(z, s_cum);
+    walk.start(cuts.begin(blockIdx.x), cuts.begin(blockIdx.x + 1));
     Item item;
     for (int qn = 0;; ++qn) {
       const bool more = walk.next(item);
-      if (!publish<C::kBlock>(p, orders, more, item, walk, total, n_pieces, s_seq, s_len) || !more)
-        break;
+      const int pieces = more && item.lo == 0 ? pieces_of(item, walk.at, cuts, blockIdx.x) : 0;
+      if (!publish<C::kBlock>(p, orders, more, item, pieces, s_seq, s_len) || !more) break;
       const bool ok =
           mbar_wait(&bar->q_empty[qn & 1], ((qn >> 1) & 1) ^ 1, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -1606,10 +1685,10 @@ cudaError_t launch_kernel(K kern, dim3 grid, int threads, int smem, bool after, 
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int D>
+template <int D, bool DEAL>
 cudaError_t launch_tiles(const Params& p, bool after, cudaStream_t stream) {
   using C = Cfg<D>;
-  auto kern = prefix_attention_kernel<D>;
+  auto kern = prefix_attention_kernel<D, DEAL>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // The register hand-over is only balanced at exactly kLaunchRegs per thread.
@@ -1648,7 +1727,12 @@ cudaError_t launch(const PrefixArgs& a, Params& p, Form form, int sms, cudaStrea
     p.z = sizes_of(a, sms, false, form);
     if (!set_maps(a, p, kBK) || !make_tmap_bf16(&p.tm_q, a.q, D, a.B * a.H * a.Lq, 1, 128))
       return cudaErrorInvalidValue;
-    if ((e = launch_tiles<D>(p, form == kMixed, stream)) != cudaSuccess) return e;
+    const int64_t items = static_cast<int64_t>(a.c.H_kv) *
+                          ((p.z.shared ? p.z.groups_p : 0) +
+                           (p.z.own ? static_cast<int64_t>(a.B) * p.z.groups_s : 0));
+    e = items > sms ? launch_tiles<D, true>(p, form == kMixed, stream)
+                    : launch_tiles<D, false>(p, form == kMixed, stream);
+    if (e != cudaSuccess) return e;
   }
   if (form == kJoint)
     return launch_kernel(join_cuts_kernel<D>, dim3(p.z.n_ctas, kGroup / 8), D * 2, 0, true, p, stream);
