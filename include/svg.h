@@ -550,8 +550,9 @@ svg_status svg_cache_reserve(const svg_cache_geom* geom, int32_t* table, int32_t
 
 /* svg_cache_write -- one layer's rows into the reserved places: the first plan[i].count
  * rows of k_new[i], v_new[i], and the rows of a replaced page that the
- * sequence keeps. May be called again with other rows while the plan and the table stand
- * (each denoising step of a chunk rewrites the chunk's rows).
+ * sequence keeps. May be called again with other rows (each denoising step of a
+ * chunk rewrites the chunk's rows) until the next call that changes the state: a replaced
+ * page may be free by then, and a sequence forked since shares the rows.
  *   seqs, plan   as given to and written by svg_cache_reserve.
  *   k_new, v_new device bf16 [n, H_kv, L, d], 16-byte aligned, not in the pool;
  *                L >= 1 rows an entry, counts above L are refused. */

@@ -240,3 +240,40 @@ def test_copy_between_pools(svg):
         assert all(torch.equal(x[i], y[j]) for i, j in ((8, 0), (2, 4), (5, 5)))
         assert not y[[1, 2, 3, 6, 7, 8]].any()
     assert svg.svg_get_device_status()[1] == 0
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_drops_table_entries_that_name_no_page_in_use(svg, in_place):
+    """Free pages below and above the number of pages in use, and pages past the pool."""
+    geom = svg.CacheGeom(40, 16, 1, 64, 3, 8)
+    refs = [0] * 40
+    for p in (0, 2, 3, 20, 39):
+        refs[p] = 1
+    #        in use           free       past the pool; none
+    table = [[0, 20, 3, 39] + [1, 4] + [40, -1],
+             [2, 39, 0, 2] + [21, 38] + [2 ** 30, -1],
+             [-1] * 8]
+    t, r = dev(table), dev(refs)
+    out = (t, r) if in_place else (torch.full_like(t, 77), torch.full_like(r, 77))
+    moves = torch.zeros(2 + 2 * 40, dtype=torch.int32, device="cuda")
+    svg.svg_cache_compact(geom, t, r, *out, moves)
+    st, bits = svg.svg_get_device_status()
+    assert st == svg.SVG_ERR_INVALID_ARG and bits == 2
+    assert moves[:6].tolist() == [2, 5, 20, 1, 39, 4]
+    assert out[0].tolist() == [[0, 1, 3, 4] + [-1] * 4, [2, 4, 0, 2] + [-1] * 4, [-1] * 8]
+    assert out[1].tolist() == [1] * 5 + [0] * 35
+
+
+def test_history_cache_refuses_a_plan_of_an_earlier_state(svg):
+    from video_dit_spatial_b200.layer import HistoryCache
+    cache = HistoryCache(1, 8, 16, 1, 1, 64, 4, 64, 2, 8)
+    k = torch.zeros((1, 1, 8, 64), dtype=torch.bfloat16, device="cuda")
+    for change in (lambda: cache.fork(dev([0]), dev([1])), lambda: cache.free(dev([1])),
+                   cache.compact, cache.reset):
+        cache.reserve(dev([0]), dev([8]))
+        cache.write(0, k, k)
+        cache.write(0, k, k)
+        change()
+        with pytest.raises(ValueError, match="follows reserve"):
+            cache.write(0, k, k)
+    assert svg.svg_get_device_status() == (svg.SVG_OK, 0)

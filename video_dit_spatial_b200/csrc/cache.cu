@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kOneThreads)
     block_sum_scan(__popc(used), warp_sums, found);
     live += found;
   }
-  int32_t* to = moves + 2 + c.n_pages;  // where each page from `live` on goes; -1: it is free
+  int32_t* to = moves + 2 + c.n_pages;  // where each page goes; -1: it is free
   int holes = 0, movers = 0;
   for (int p0 = 0; p0 < c.n_pages; p0 += kStep) {
     const int mine = p0 + tid * kPer;
@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kOneThreads)
     at = movers + block_sum_scan(__popc(mover), warp_sums, found) - __popc(mover);
     for (; mover != 0; mover &= mover - 1) moves[2 + 2 * at++] = mine + __ffs(mover) - 1;
     movers += found;
-    for (int k = below; k < kPer && mine + k < c.n_pages; ++k) to[mine + k] = -1;
+    for (int k = 0; k < kPer && mine + k < c.n_pages; ++k)
+      to[mine + k] = k < below && (used >> k & 1u) ? mine + k : -1;
   }
   __syncthreads();
   for (int i = tid; i < movers; i += kOneThreads) to[moves[2 + 2 * i]] = moves[3 + 2 * i];
@@ -331,8 +332,8 @@ __global__ void cache_renumber_kernel(CacheDims c, const int32_t* table, const i
   const int64_t n = static_cast<int64_t>(c.max_seqs) * c.max_pages;
   for (int64_t i = i0; i < n; i += step) {
     const int p = table[i];
-    const int q = p >= live && p < c.n_pages ? to[p] : p;
-    if (p >= 0 && (q < 0 || q >= c.n_pages)) atomicOr(status, kDevErrBounds);  // not a page in use
+    const int q = p < 0 ? p : p < c.n_pages ? to[p] : -1;
+    if (q < 0 && p >= 0) flag(status, kDevErrBounds);  // not a page in use
     table_out[i] = q;
   }
   for (int64_t i = i0; i < n_moves; i += step) {

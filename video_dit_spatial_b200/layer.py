@@ -331,7 +331,8 @@ class HistoryCache:
 
       reserve(seqs, counts)     room for a chunk's rows in every sequence of the batch
       write(layer, k, v)        a layer's keys and values of the chunk (again at
-                                each denoising step: the rows are overwritten)
+                                each denoising step: the rows are overwritten),
+                                until the next fork, free, reset or compact
       attend(layer, q, ...)     the chunk's queries over the shared history and
                                 each sequence's own rows
       fork(src, dst)            continuations of one history, sharing its pages
@@ -372,14 +373,17 @@ class HistoryCache:
     def reset(self, stream=None) -> None:
         from . import svg_cache_reset
         svg_cache_reset(self.geom, *self._state, stream=stream)
+        self._seqs = None  # the plan is of the state before
 
     def fork(self, src, dst, stream=None) -> None:
         from . import svg_cache_fork
         svg_cache_fork(self.geom, *self._state, src, dst, stream=stream)
+        self._seqs = None  # a target may share the rows of the plan
 
     def free(self, seqs, keep=None, stream=None) -> None:
         from . import svg_cache_free
         svg_cache_free(self.geom, *self._state, seqs, keep, stream=stream)
+        self._seqs = None  # the plan's rows may be gone
 
     def reserve(self, seqs, counts, stream=None) -> None:
         from . import svg_cache_reserve
@@ -390,7 +394,7 @@ class HistoryCache:
         """k_new, v_new [n, H_kv, L, d]: the rows that the last reserve made room for."""
         from . import svg_cache_write
         if self._seqs is None:
-            raise ValueError("write follows reserve")
+            raise ValueError("write follows reserve, with no fork, free, reset or compact between")
         svg_cache_write(self.geom, self.table, self._seqs, self.plan, k_new.shape[2], k_new, v_new,
                         *self.pools[layer], stream=stream)
 
