@@ -98,7 +98,8 @@ struct Pieces {
 };
 
 struct __align__(64) Params {
-  CUtensorMap tm_k, tm_v, tm_q;  // tm_q: the rows of q, for items of one sequence
+  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_q, tm_q_rows;  // the rows of q in boxes of 128, for items of one sequence, and one by one
   CacheDims c;
   Sizes z;
   int32_t prefix_seq;
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     prefetch_tensormap(&p.tm_k);
     prefetch_tensormap(&p.tm_v);
-    prefetch_tensormap(&p.tm_q);
+    prefetch_tensormap(z.shared ? &p.tm_q_rows : &p.tm_q);
   }
 
   Cuts cuts;
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 32) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bar->q_full[s], 32);
+      mbar_init(&bar->q_full[s], 1);
       mbar_init(&bar->q_empty[s], 1);
       mbar_init(&bar->s_full[s], 1);
       mbar_init(&bar->s_free[s], 4);  // warps
@@ -834,12 +835,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ---------------------------------------------------------- query rows
       // The rows of one sequence are one run of q: a tiled load (what it brings of
-      // other rows past the item's end is never used). Gathered rows come by
-      // 16-byte copies to the same swizzled places.
+      // other rows past the item's end is never used). The rows of several are
+      // gathered, four to a lane. (Copied by cp.async to the same places, 64 to a lane, they
+      // took 5k cycles a tile, in which nothing else can begin.)
       const int lane = lane_id();
-      constexpr int kVecs = D / 8;  // 16-byte vectors of a row
-      const uint32_t q_addr = smem_u32(sQ);
-      const int vec = lane % kVecs;
       int qn = 0;
       bool ok = true;
       Walk walk(z, s_cum);
@@ -867,39 +866,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = more = false;
             break;
           }
+          uint8_t* dst = sQ + (qn & 1) * C::kTile;
           if (!item.shared) {
             if (lane == 0) {
               const int64_t row = q_row(z, item, r0);
               mbar_arrive_expect_tx(full, C::kTile);
               for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_3d(sQ + (qn & 1) * C::kTile + pn * C::kPanel, &p.tm_q, full, pn * 64,
-                            static_cast<int>(row), 0);
-            } else {
-              mbar_arrive(full);
+                tma_load_3d(dst + pn * C::kPanel, &p.tm_q, full, pn * 64, static_cast<int>(row), 0);
             }
             continue;
           }
-          // lane i finds the rows i, i + 32, ... and hands them round
-          const uint32_t dst = q_addr + (qn & 1) * C::kTile + (vec >> 3) * C::kPanel;
-          const int rows = min(item.rows - r0, 128);
-          for (int r1 = 0; r1 < rows; r1 += 32) {
-            const int mine = r1 + lane < rows ? static_cast<int>(q_row(z, item, r0 + r1 + lane)) : 0;
-#pragma unroll 8
-            for (int i = lane / kVecs; i < 32; i += 32 / kVecs) {
-              const int src = __shfl_sync(0xffffffffu, mine, i);
-              const int r = r1 + i;
-              if (r < rows)
-                cp_async16(dst + r * 128 + (((vec & 7) ^ (r & 7)) << 4),
-                           p.q + static_cast<int64_t>(src) * D + vec * 8);
-            }
+          const int fours = (min(item.rows - r0, 128) + 3) / 4;
+          if (lane == 0) mbar_arrive_expect_tx(full, fours * 4 * 128 * C::kPanels);
+          __syncwarp();
+          if (lane < fours) {
+            int row[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)  // past the item's end its last row again, not used
+              row[i] = static_cast<int>(q_row(z, item, min(r0 + 4 * lane + i, item.rows - 1)));
+#pragma unroll
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              tma_gather4(dst + pn * C::kPanel + lane * 512, &p.tm_q_rows, full, pn * 64, row[0],
+                          row[1], row[2], row[3]);
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          mbar_arrive(full);
         }
       }
       if (*abort_flag && lane == 0) {
-        // Let the tiled loads this warp started land before the CTA retires.
+        // Let the loads this warp started land before the CTA retires.
         for (int j = (qn > 2 ? qn - 2 : 0); j < qn; ++j) {
           const long long t0 = clock64();
           while (!mbar_try_wait(&bar->q_full[j & 1], (j >> 1) & 1) &&
@@ -1725,7 +1718,10 @@ cudaError_t launch(const PrefixArgs& a, Params& p, Form form, int sms, cudaStrea
   }
   if (form != kFew) {
     p.z = sizes_of(a, sms, false, form);
-    if (!set_maps(a, p, kBK) || !make_tmap_bf16(&p.tm_q, a.q, D, a.B * a.H * a.Lq, 1, 128))
+    if (!set_maps(a, p, kBK) ||
+        (p.z.own && !make_tmap_bf16(&p.tm_q, a.q, D, a.B * a.H * a.Lq, 1, 128)) ||
+        (p.z.shared &&
+         !make_tmap_rows_bf16(&p.tm_q_rows, a.q, D, static_cast<int64_t>(a.B) * a.H * a.Lq)))
       return cudaErrorInvalidValue;
     const int64_t items = static_cast<int64_t>(a.c.H_kv) *
                           ((p.z.shared ? p.z.groups_p : 0) +
