@@ -73,6 +73,7 @@ struct Sizes {
   int32_t groups_p, groups_s;    // row groups of a shared item's key head, of a sequence
   int32_t cost_p, cost_s;        // cost of one block over all those groups
   int64_t shared_cost;           // of all shared items, also where another kernel has them
+  int32_t shared_items;          // of the tile kernel
   int32_t mixed;                 // 1: the other kind of items is another kernel's, at the same time
 };
 
@@ -383,17 +384,20 @@ __host__ __device__ inline int64_t rest_begin(const Sizes& z, const int64_t* cum
          before;
 }
 
-// SMs that the few-row kernel takes of n while the tile kernel has the rest: as the
-// cycles of their work, some 1000 for one of its blocks, 2000 for an item's beginning
-// and end, and 1000 for a unit of the tile kernel's cost. Both kernels are
-// launched with n CTAs and those past their share leave at once, since the lengths
-// are not known on the host. At d = 128, one kernel after the other and side by
-// side: rows of 64 sequences over 20001 shared rows and up to 700 of their own,
-// four query heads to a key head, 79 and 61 us; of 40 over 20000 and 64, 24 heads, 82 and 68 us.
-__device__ __forceinline__ int few_share(int n, int64_t blocks, int64_t items, int64_t tile_cost) {
+// SMs that the few-row kernel takes of n while the tile kernel has the rest: as the time of
+// their work. In units of the tile kernel's cost (0.5 us): one of the few-row kernel's blocks 3/2,
+// an item's beginning and end 1, one of the tile kernel's items 8 beside its blocks. Both
+// kernels are launched with n CTAs and those past their share leave at once, since the
+// lengths are not known on the host. At d = 128, one kernel after the other and side by
+// side: rows of 64 sequences over 20001 shared rows and up to 700 of their own, four
+// query heads to a key head, 79 and 59 us; of 40 over 20000 and 64, 24 heads, 82 and 70 us.
+// (Without the tile kernel's items: rows of 150 over 700 and up to 30, eight heads to a key
+// head, 54 us instead of 47.)
+__device__ __forceinline__ int few_share(int n, int64_t blocks, int64_t items, int64_t tile_cost,
+                                         int tile_items) {
   if (blocks == 0) return 0;
-  const int64_t few = blocks + 2 * items;
-  const int64_t s = n * few / (few + tile_cost);
+  const int64_t few = 3 * blocks + 2 * items;
+  const int64_t s = n * few / (few + 2 * (tile_cost + 8 * tile_items));
   return s < 1 ? 1 : s > n - 1 ? n - 1 : static_cast<int>(s);
 }
 
@@ -446,7 +450,7 @@ __device__ __forceinline__ bool plan_pieces(const Params& p, int64_t* s_cum, int
   const int64_t shared = ok_prefix ? z.shared_cost : 0;
   int n = z.n_ctas;
   if (z.mixed) {
-    const int few = few_share(n, own, s_cum[z.B + 1] * z.H_kv, shared);
+    const int few = few_share(n, own, s_cum[z.B + 1] * z.H_kv, shared, z.shared_items);
     n = z.own ? few : n - few;
   }
   cuts.total = (z.own ? own * z.cost_s : 0) + (z.shared ? shared : 0);
@@ -1655,6 +1659,7 @@ Sizes sizes_of(const PrefixArgs& a, int n_ctas, bool few, Form form) {
   z.cost_p = group_cost(a.B * GL, group);
   z.cost_s = group_cost(GL, group);
   // the tile kernel's, but where the few-row kernel has all
+  z.shared_items = a.c.H_kv * groups(a.B * GL, kGroup);
   z.shared_cost = form == kFew ? static_cast<int64_t>(z.nbp) * z.cost_p * z.H_kv
                                : static_cast<int64_t>((a.prefix_len + kBK - 1) / kBK) *
                                      group_cost(a.B * GL, kGroup) * z.H_kv;
