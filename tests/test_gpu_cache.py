@@ -277,3 +277,24 @@ def test_history_cache_refuses_a_plan_of_an_earlier_state(svg):
         with pytest.raises(ValueError, match="follows reserve"):
             cache.write(0, k, k)
     assert svg.svg_get_device_status() == (svg.SVG_OK, 0)
+
+
+def test_history_cache_refuses_other_shapes(svg):
+    from video_dit_spatial_b200.layer import HistoryCache
+    cache = HistoryCache(1, 8, 16, 4, 2, 64, 4, 64, 2, 8)
+    seqs = dev([0, 1])
+    new = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    cache.reserve(seqs, dev([8, 8]))
+    cache.write(0, new(2, 2, 8, 64), new(2, 2, 8, 64))
+    for k, v in ((new(2, 4, 8, 64), new(2, 4, 8, 64)), (new(2, 2, 8, 128), new(2, 2, 8, 128)),
+                 (new(3, 2, 8, 64), new(3, 2, 8, 64)), (new(2, 2, 8, 64), new(2, 2, 9, 64))):
+        with pytest.raises(ValueError, match="rows of shape"):
+            cache.write(0, k, v)
+    q, o, lse = new(2, 4, 8, 64), new(2, 4, 8, 64), torch.zeros((2, 4, 8), device="cuda")
+    cache.attend(0, q, seqs, 0, 0, o, lse)
+    assert torch.all(o == 0) and torch.all((lse - np.log(8.0)).abs() < 1e-5)
+    for bad in ((new(2, 8, 8, 64), new(2, 8, 8, 64), None), (q, new(2, 4, 9, 64), None),
+                (new(3, 4, 8, 64), new(3, 4, 8, 64), None), (q, o, lse[:, :, :4])):
+        with pytest.raises(ValueError, match="queries of shape"):
+            cache.attend(0, bad[0], seqs, 0, 0, *bad[1:])
+    assert svg.svg_get_device_status() == (svg.SVG_OK, 0)

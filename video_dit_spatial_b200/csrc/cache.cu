@@ -6,8 +6,10 @@
 // zero; there is no free list, so nothing has to be kept in order: pages are
 // handed out lowest number first, which makes every call's result depend on
 // the state and its arguments alone. The bookkeeping kernels touch integers
-// only and are bound by the latency of a few dependent loads (2 to 5 us); the
-// two kernels that move rows are bound by HBM.
+// only and are bound by the latency of a few dependent loads (2 to 5 us, with many
+// sequences of many shared pages by the atomics on their counts); the two
+// kernels that move rows are bound by HBM: 709 MB written in 103 us (6.9 TB/s, the last of
+// it into L2), 1.57 GB of pages copied in 242 us (6.5 TB/s).
 #include "internal.h"
 #include "sm100.cuh"
 

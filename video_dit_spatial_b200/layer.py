@@ -395,6 +395,12 @@ class HistoryCache:
         from . import svg_cache_write
         if self._seqs is None:
             raise ValueError("write follows reserve, with no fork, free, reset or compact between")
+        n, H_kv, _, d = k_new.shape
+        if v_new.shape != k_new.shape or H_kv != self.geom.H_kv or d != self.geom.head_dim \
+                or n != self._seqs.numel():
+            raise ValueError(f"rows of shape {tuple(k_new.shape)} and {tuple(v_new.shape)} for "
+                             f"{self._seqs.numel()} sequences, {self.geom.H_kv} heads of "
+                             f"{self.geom.head_dim}")
         svg_cache_write(self.geom, self.table, self._seqs, self.plan, k_new.shape[2], k_new, v_new,
                         *self.pools[layer], stream=stream)
 
@@ -411,6 +417,11 @@ class HistoryCache:
                stream=None) -> None:
         """q, o [B, H, Lq, d]; the first prefix_len rows of prefix_seq are shared by all."""
         from . import svg_prefix_attention
+        B, H, Lq, d = q.shape
+        if o.shape != q.shape or H != self.H or d != self.geom.head_dim or B != seqs.numel() \
+                or (lse is not None and lse.shape != q.shape[:3]):
+            raise ValueError(f"queries of shape {tuple(q.shape)}, outputs of shape {tuple(o.shape)} "
+                             f"for {seqs.numel()} sequences, {self.H} heads of {self.geom.head_dim}")
         svg_prefix_attention(self.geom, q.shape[0], self.H, q.shape[2], prefix_seq, prefix_len,
                              self.scale, q, *self.pools[layer], self.table, self.lens, seqs, o,
                              lse, self.workspace, stream=stream)
