@@ -122,6 +122,17 @@ def test_binding_refuses_host_tensors(svg):
         svg.svg_cache_reset(g, table, table, table)
 
 
+def test_attention_refuses_tables_of_longer_rows(svg):
+    """Above 2^24 rows the bookkeeping goes on, the attention does not."""
+    for ps in (16, 256):
+        fits, over = (1 << 24) // ps, (1 << 24) // ps + 1
+        assert svg.svg_prefix_attention_workspace_bytes(_geom(svg, page_size=ps, max_pages=fits),
+                                                        2, 4, 3) > 0
+        with pytest.raises(svg.SvgError) as e:
+            svg.svg_prefix_attention_workspace_bytes(_geom(svg, page_size=ps, max_pages=over), 2, 4, 3)
+        assert e.value.status == svg.SVG_ERR_INVALID_ARG
+
+
 # ---------------------------------------------------------------- the oracle
 def test_model_by_hand():
     m = CO.CacheModel(n_pages=6, page_size=16, H_kv=1, d=2, max_seqs=3, max_pages=3)

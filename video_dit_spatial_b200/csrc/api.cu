@@ -878,6 +878,9 @@ static svg_status check_prefix_shape(const svg_cache_geom* geom, svg::CacheDims*
   if (st != SVG_OK) return st;
   if (B < 1 || B > 1024 || H < 1 || Lq < 1 || H % c->H_kv != 0) return SVG_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * H > 0x7fffffffLL / Lq) return SVG_ERR_INVALID_ARG;
+  // Of longer rows the fp32 sums would lose more than the output's rounding, and the bounded
+  // waits for the end of a CTA's piece of one might run out.
+  if (c->max_rows() > (1 << 24)) return SVG_ERR_INVALID_ARG;
   return SVG_OK;
 }
 
