@@ -615,8 +615,9 @@ svg_status svg_prefix_attention_workspace_bytes(const svg_cache_geom* geom, int3
  * pool sets it too, and its rows count as zeros.
  * Same results on every call: no atomics in the arithmetic.
  * Errors: as above, and INVALID_ARG (B < 1 or > 1024, Lq < 1, H not a multiple
- * of H_kv, B * H * Lq > 2^31 - 1, max_pages * page_size > 2^24, prefix_len not in [0, max_pages * page_size],
- * prefix_seq not in [0, max_seqs), scale), CAPACITY (workspace). */
+ * of H_kv, B * H * Lq > 2^31 - 1, max_pages * page_size > 2^20 (further than
+ * fp32 sums reach), prefix_len not in [0, max_pages * page_size], prefix_seq not
+ * in [0, max_seqs), scale), CAPACITY (workspace). */
 svg_status svg_prefix_attention(const svg_cache_geom* geom, int32_t B, int32_t H, int32_t Lq,
                                 int32_t prefix_seq, int32_t prefix_len, float scale,
                                 const svg_bf16* q, const svg_bf16* k_pages,

@@ -123,9 +123,9 @@ def test_binding_refuses_host_tensors(svg):
 
 
 def test_attention_refuses_tables_of_longer_rows(svg):
-    """Above 2^24 rows the bookkeeping goes on, the attention does not."""
+    """Above 2^20 rows the bookkeeping goes on, the attention does not."""
     for ps in (16, 256):
-        fits, over = (1 << 24) // ps, (1 << 24) // ps + 1
+        fits, over = (1 << 20) // ps, (1 << 20) // ps + 1
         assert svg.svg_prefix_attention_workspace_bytes(_geom(svg, page_size=ps, max_pages=fits),
                                                         2, 4, 3) > 0
         with pytest.raises(svg.SvgError) as e:

@@ -183,6 +183,43 @@ def test_more_items_than_sms(svg, name, idle):
     Case(svg, *DEALT[name], seed=17, idle=idle).call(svg).compare(name)
 
 
+@pytest.mark.parametrize("d,H,H_kv,Lq", [(64, 160, 160, 17), (128, 4, 2, 200), (128, 8, 4, 1),
+                                         (64, 200, 200, 1)])
+def test_the_longest_table(svg, d, H, H_kv, Lq):
+    """2^20 rows, the same seven pages over and over: the answer is that of one round of them
+    and the sum 585 times as large. Sums of one sign at a time are where rounding adds up: O
+    takes 16 keys at a time, 2^16 sums that lose up to 2^-24 each, so 2^-8 of `spread`; the
+    row sum 2^14 of them (a key pair at a time within a block, then block by block), 2^-10."""
+    ps, n_pages = 256, 7
+    W = (1 << 20) // ps
+    rounds = W // n_pages
+    n = rounds * n_pages * ps
+    g = torch.Generator().manual_seed(d + H)
+    k, v = (torch.randn((n_pages, H_kv, ps, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((1, H, Lq, d), generator=g).to(torch.bfloat16)
+    table = (torch.arange(W, dtype=torch.int32) % n_pages).repeat(2, 1)
+    geom = svg.CacheGeom(n_pages, ps, H_kv, d, 2, W)
+    o = torch.empty((1, H, Lq, d), dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty((1, H, Lq), device="cuda")
+    ws = torch.empty(svg.svg_prefix_attention_workspace_bytes(geom, 1, H, Lq), dtype=torch.uint8,
+                     device="cuda")
+    svg.svg_prefix_attention(geom, 1, H, Lq, 0, n, d ** -0.5, q.cuda(), k.cuda(), v.cuda(),
+                             table.cuda(), dev([n, n]), dev([1]), o, lse, ws)
+    assert svg.svg_get_device_status() == (svg.SVG_OK, 0)
+    kk, vv = (x.transpose(0, 1).reshape(H_kv, -1, d).repeat_interleave(H // H_kv, 0).double()
+              for x in (k, v))
+    z = q[0].double() @ kk.transpose(1, 2) * float(np.float32(d ** -0.5))
+    w = torch.softmax(z, -1)
+    want, spread = w @ vv, w @ vv.abs()
+    want_lse = torch.logsumexp(z, -1) + np.log(rounds)
+    X = float(q.double().norm(dim=-1).max() * kk.norm(dim=-1).max()) * d ** -0.5
+    soft = 2.0 ** -8 + 2.0 ** -8 + 2.0 ** -10 + 2.0 ** -19 * (1 + X)
+    assert torch.all((o[0].cpu().double() - want).abs() <=
+                     soft * spread * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs())
+    assert torch.all((lse[0].cpu().double() - want_lse).abs() <=
+                     2.0 ** -10 + 2.0 ** -19 * (1 + X) + 2.0 ** -22 * want_lse.abs())
+
+
 @pytest.mark.parametrize("name", ["grouped", "tiles_cross_sequences", "rows_257"])
 def test_idle_entries_keep_their_rows(svg, name):
     a = CASES[name]

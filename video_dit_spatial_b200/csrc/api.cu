@@ -878,9 +878,10 @@ static svg_status check_prefix_shape(const svg_cache_geom* geom, svg::CacheDims*
   if (st != SVG_OK) return st;
   if (B < 1 || B > 1024 || H < 1 || Lq < 1 || H % c->H_kv != 0) return SVG_ERR_INVALID_ARG;
   if (static_cast<int64_t>(B) * H > 0x7fffffffLL / Lq) return SVG_ERR_INVALID_ARG;
-  // Of longer rows the fp32 sums would lose more than the output's rounding, and the bounded
-  // waits for the end of a CTA's piece of one might run out.
-  if (c->max_rows() > (1 << 24)) return SVG_ERR_INVALID_ARG;
+  // O grows by 16 keys at a time: of 2^20 keys that is 2^16 sums in fp32, which may lose 2^-8 of
+  // it between them, as much as the output's rounding does. (2^24 keys in one piece, the
+  // same 1792 over and over: 1.5e-2 off.)
+  if (c->max_rows() > (1 << 20)) return SVG_ERR_INVALID_ARG;
   return SVG_OK;
 }
 

@@ -346,7 +346,7 @@ class HistoryCache:
 
     def __init__(self, n_layers: int, n_pages: int, page_size: int, H: int, H_kv: int, d: int,
                  max_seqs: int, max_rows: int, batch: int, rows: int, scale=None, device="cuda"):
-        """max_rows: of one sequence; batch, rows: the most sequences and query
+        """max_rows: of one sequence, at most 2^20; batch, rows: the most sequences and query
         rows a sequence that one call of reserve, write or attend has."""
         from . import CacheGeom, svg_cache_reset, svg_prefix_attention_workspace_bytes
         self.geom = CacheGeom(n_pages, page_size, H_kv, d, max_seqs, -(-max_rows // page_size))
