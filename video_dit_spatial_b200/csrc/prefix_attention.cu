@@ -5,7 +5,9 @@
 // pass over the keys with a running maximum and sum per row. Two disjoint key
 // sets give (O, m, l) each, joined exactly by
 //   m = max(m1, m2), l = sum l_k 2^(m_k - m), O = sum O_k 2^(m_k - m) / l,
-// which is what makes the work divisible along the keys.
+// which is what makes the work divisible along the keys. A NaN score leaves the
+// maximum alone (a maximum skips NaN) and makes l and O NaN, and nothing after it takes them
+// for anything else: "no key" is l = 0, not a maximum of -inf, which a row of NaN has too.
 //
 // Work. With G = H / H_kv query heads to a key head, the G * Lq query rows of
 // (sequence b, key head) are contiguous in q. Items, each a group of up to 256
@@ -227,6 +229,13 @@ struct FewCfg {
 };
 
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
+
+// 1 / l and the natural log-sum-exp of a row with maximum m (log2 units) and sum l. No weight
+// at all is O = 0, lse = -inf; NaN stays NaN.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
 
 // Length of entry b's sequence, -1 where the entry is idle, -2 where it is refused.
 __device__ __forceinline__ int entry_len(const CacheDims& c, const int32_t* lens, int seq) {
@@ -1081,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           static_cast<int64_t>(it.lo > 0 || z.joint ? cta : it.id) * part.stride;
       float4* out = (it.lo > 0 ? part.head_o : part.first_o) + slot * (D / 4) + rr;
       float2* out_ml = (it.lo > 0 ? part.head_ml : part.first_ml) + slot + rr;
-      const float inv_l = l > 0.0f ? 1.0f / l : 0.0f;
+      const float inv_l = inverse_sum(l);
       // two tiles: all columns of this tile's O; one tile: this warpgroup's half of both
       const int c_lo = two ? 0 : t * (D / 2), c_n = two ? D : D / 2;
       if (active) {
@@ -1132,7 +1141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!final_rows) {
           *out_ml = make_float2(m, l);
         } else if (p.lse != nullptr) {
-          p.lse[row] = l > 0.0f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+          p.lse[row] = log_sum(m, l);
         }
       }
       if (tid == 0) {
@@ -1481,7 +1490,6 @@ __device__ __forceinline__ void join_one(Joined& s, float2 ml, float4 x) {
   const float m = fmaxf(s.m, ml.x);
   const float m_use = m == -INFINITY ? 0.0f : m;
   const float a = fast_exp2(s.m - m_use), b = fast_exp2(ml.x - m_use);
-  if (ml.x == -INFINITY) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);  // no key: nothing was summed
   s.o = make_float4(s.o.x * a + x.x * b, s.o.y * a + x.y * b, s.o.z * a + x.z * b,
                     s.o.w * a + x.w * b);
   s.l = s.l * a + ml.y * b;
@@ -1490,11 +1498,11 @@ __device__ __forceinline__ void join_one(Joined& s, float2 ml, float4 x) {
 
 template <int D>
 __device__ __forceinline__ void store_row(const Params& p, int64_t row, int c4, const Joined& s) {
-  const float inv = s.l > 0.0f ? 1.0f / s.l : 0.0f;
+  const float inv = inverse_sum(s.l);
   *reinterpret_cast<uint2*>(p.o + row * D + c4 * 4) =
       make_uint2(pack_bf16x2(s.o.x * inv, s.o.y * inv), pack_bf16x2(s.o.z * inv, s.o.w * inv));
   if (p.lse != nullptr && c4 == 0)
-    p.lse[row] = s.l > 0.0f ? (s.m + __log2f(s.l)) * 0.69314718055994531f : -INFINITY;
+    p.lse[row] = log_sum(s.m, s.l);
 }
 
 // Pieces k = first, first + step, ... of row r of an item. (A count that cannot be, where a
