@@ -1,0 +1,47 @@
+"""HistoryCache without a GPU: what it gives to the calls below it, which are recorded."""
+import pytest
+import torch
+
+import video_dit_spatial_b200 as svg
+from video_dit_spatial_b200.layer import HistoryCache
+
+CALLS = ("svg_cache_reset", "svg_cache_fork", "svg_cache_free", "svg_cache_reserve",
+         "svg_cache_write", "svg_cache_compact", "svg_cache_copy_pages", "svg_prefix_attention")
+
+
+@pytest.fixture()
+def calls(monkeypatch):
+    """The calls made, in order: (name, copies of the tensors among the arguments, keywords)."""
+    made = []
+
+    def record(name):
+        def call(*args, **kw):
+            made.append((name, [x.clone() if torch.is_tensor(x) else x for x in args], kw))
+        return call
+
+    for name in CALLS:
+        monkeypatch.setattr(svg, name, record(name))
+    monkeypatch.setattr(svg, "svg_prefix_attention_workspace_bytes", lambda *a: 256)
+    return made
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def test_write_names_the_sequences_that_reserve_was_given(calls):
+    cache = HistoryCache(2, 8, 16, 2, 1, 64, 6, 64, 3, 8, device="cpu")
+    seqs, rows = ints([0, 4]), torch.zeros((2, 1, 8, 64), dtype=torch.bfloat16)
+    cache.reserve(seqs, ints([8, 3]))
+    seqs.copy_(ints([2, 3]))
+    cache.write(0, rows, rows)
+    del seqs
+    cache.write(1, rows, rows)
+    assert [(name, args[2].tolist()) for name, args, _ in calls if name == "svg_cache_write"] == \
+        [("svg_cache_write", [0, 4])] * 2
+    cache.reserve(ints([1]), ints([1]))
+    with pytest.raises(ValueError, match="rows of shape"):
+        cache.write(0, rows, rows)
+    cache.fork(ints([0]), ints([5]))
+    with pytest.raises(ValueError, match="follows reserve"):
+        cache.write(0, rows[:1], rows[:1])

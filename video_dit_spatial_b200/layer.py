@@ -321,6 +321,13 @@ class SemanticSparseLayer:
         self.attend(q, k, v, o, lse, stream)
 
 
+def _on_stream(stream):
+    """Context in which torch works on `stream`: a stream, its handle, or None for the current one."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    return torch.cuda.stream(stream)
+
+
 class HistoryCache:
     """Keys and values of the frames made so far, and attention over them.
 
@@ -359,11 +366,12 @@ class HistoryCache:
         self.table = torch.empty((max_seqs, self.geom.max_pages), **i32)
         self.lens, self.refs = torch.empty(max_seqs, **i32), torch.empty(n_pages, **i32)
         self.plan = torch.empty((batch, 4), **i32)
+        self._numbers = torch.empty(batch, **i32)  # of the sequences the plan is for
         self.moves = torch.empty(2 + 2 * n_pages, **i32)
         shape = (n_pages, H_kv, page_size, d)
         mk = lambda: torch.empty(shape, dtype=torch.bfloat16, device=dev)  # noqa: E731
         self.pools = [(mk(), mk()) for _ in range(n_layers)]
-        self._seqs = None
+        self._planned = 0  # entries of the plan; 0: none, or one of an earlier state
         svg_cache_reset(self.geom, self.table, self.lens, self.refs)
 
     @property
@@ -373,36 +381,40 @@ class HistoryCache:
     def reset(self, stream=None) -> None:
         from . import svg_cache_reset
         svg_cache_reset(self.geom, *self._state, stream=stream)
-        self._seqs = None  # the plan is of the state before
+        self._planned = 0  # the plan is of the state before
 
     def fork(self, src, dst, stream=None) -> None:
         from . import svg_cache_fork
         svg_cache_fork(self.geom, *self._state, src, dst, stream=stream)
-        self._seqs = None  # a target may share the rows of the plan
+        self._planned = 0  # a target may share the rows of the plan
 
     def free(self, seqs, keep=None, stream=None) -> None:
         from . import svg_cache_free
         svg_cache_free(self.geom, *self._state, seqs, keep, stream=stream)
-        self._seqs = None  # the plan's rows may be gone
+        self._planned = 0  # the plan's rows may be gone
 
     def reserve(self, seqs, counts, stream=None) -> None:
         from . import svg_cache_reserve
         svg_cache_reserve(self.geom, *self._state, seqs, counts, self.plan, stream=stream)
-        self._seqs = seqs
+        # write pairs the plan with these numbers, whatever the caller's list holds by then
+        n = seqs.numel()
+        with _on_stream(stream):
+            self._numbers[:n].copy_(seqs.view(-1))
+        self._planned = n
 
     def write(self, layer: int, k_new, v_new, stream=None) -> None:
         """k_new, v_new [n, H_kv, L, d]: the rows that the last reserve made room for."""
         from . import svg_cache_write
-        if self._seqs is None:
+        if not self._planned:
             raise ValueError("write follows reserve, with no fork, free, reset or compact between")
         n, H_kv, _, d = k_new.shape
         if v_new.shape != k_new.shape or H_kv != self.geom.H_kv or d != self.geom.head_dim \
-                or n != self._seqs.numel():
+                or n != self._planned:
             raise ValueError(f"rows of shape {tuple(k_new.shape)} and {tuple(v_new.shape)} for "
-                             f"{self._seqs.numel()} sequences, {self.geom.H_kv} heads of "
+                             f"{self._planned} sequences, {self.geom.H_kv} heads of "
                              f"{self.geom.head_dim}")
-        svg_cache_write(self.geom, self.table, self._seqs, self.plan, k_new.shape[2], k_new, v_new,
-                        *self.pools[layer], stream=stream)
+        svg_cache_write(self.geom, self.table, self._numbers[:n], self.plan, k_new.shape[2], k_new,
+                        v_new, *self.pools[layer], stream=stream)
 
     def compact(self, stream=None) -> None:
         from . import svg_cache_compact, svg_cache_copy_pages
@@ -411,7 +423,7 @@ class HistoryCache:
         for k, v in self.pools:
             svg_cache_copy_pages(self.geom, self.moves, self.geom.n_pages, k, v, k, v,
                                  stream=stream)
-        self._seqs = None  # the plan names pages by their old numbers
+        self._planned = 0  # the plan names pages by their old numbers
 
     def attend(self, layer: int, q, seqs, prefix_seq: int, prefix_len: int, o, lse=None,
                stream=None) -> None:
