@@ -497,8 +497,9 @@ svg_status svg2_sparse_attention(int32_t BH, int32_t N, int32_t d, int32_t block
  *           [0, max_seqs). A negative number is an idle entry (a padded
  *           batch) and does nothing. An entry refused on the device sets the
  *           bounds bit and changes nothing: a number past the end, a sequence
- *           named twice (the first one counts), a length or page in the state
- *           that cannot be.
+ *           named twice (the first one counts), a length in the state or a plan that
+ *           cannot be, or a page number that cannot be where fork would share
+ *           the page or reserve and write would replace it.
  * Order     calls on one state and the layers' pools are ordered by their
  *           stream; two streams need the caller's own ordering.
  * Errors    INVALID_ARG (null, misaligned, sizes < 1, n > 1024, n_pages > 2^24,
@@ -528,7 +529,8 @@ svg_status svg_cache_fork(const svg_cache_geom* geom, int32_t* table, int32_t* l
 /* svg_cache_free -- sequence seqs[i] keeps its first keep[i] rows (device int32
  * [n]; NULL: none); the pages past them are given up and are free once no
  * sequence holds them. keep[i] at or above the length changes nothing, a negative one is
- * refused. */
+ * refused. A page number that cannot be, or of a page that no sequence holds, sets the bounds bit
+ * and is passed over, so that a sequence with one can be dropped. */
 svg_status svg_cache_free(const svg_cache_geom* geom, int32_t* table, int32_t* lens,
                           int32_t* refs, const int32_t* seqs, const int32_t* keep, int32_t n,
                           svg_stream_t stream);
@@ -555,7 +557,8 @@ svg_status svg_cache_reserve(const svg_cache_geom* geom, int32_t* table, int32_t
  * page may be free by then, and a sequence forked since shares the rows.
  *   seqs, plan   as given to and written by svg_cache_reserve.
  *   k_new, v_new device bf16 [n, H_kv, L, d], 16-byte aligned, not in the pool;
- *                L >= 1 rows an entry, counts above L are refused. */
+ *                L >= 1 rows an entry, counts above L are refused. A row whose page number
+ *                cannot be sets the bounds bit and is left out. */
 svg_status svg_cache_write(const svg_cache_geom* geom, const int32_t* table, const int32_t* seqs,
                            const int32_t* plan, int32_t n, int32_t L, const svg_bf16* k_new,
                            const svg_bf16* v_new, svg_bf16* k_pages, svg_bf16* v_pages,

@@ -61,16 +61,21 @@ __global__ void __launch_bounds__(kSeqThreads)
   const int used = (len + c.ps - 1) / c.ps;
   const int32_t* from = table + static_cast<int64_t>(s) * c.max_pages;
   int32_t* to = table + static_cast<int64_t>(t) * c.max_pages;
+  // A page number that cannot be refuses the entry: all are looked at before the first is copied.
+  const int p0 = tid < used ? from[tid] : 0;
   for (int k = tid; k < used; k += kSeqThreads) {
-    const int p = from[k];
-    to[k] = p;
-    if (p >= 0 && p < c.n_pages) {
-      atomicAdd(refs + p, 1);
-    } else {
-      flag(status, kDevErrBounds);
-    }
+    const int p = k == tid ? p0 : from[k];
+    bad = bad || p < 0 || p >= c.n_pages;
   }
-  __syncthreads();  // every thread has read lens[t]
+  if (__syncthreads_or(bad)) {  // every thread has read lens[t], too
+    if (tid == 0) flag(status, kDevErrBounds);
+    return;
+  }
+  for (int k = tid; k < used; k += kSeqThreads) {
+    const int p = k == tid ? p0 : from[k];
+    to[k] = p;
+    atomicAdd(refs + p, 1);
+  }
   if (tid == 0) lens[t] = len;
 }
 
@@ -374,12 +379,13 @@ __global__ void __launch_bounds__(kRowThreads)
   const bool copy = static_cast<int>(blockIdx.x) >= new_chunks;
   const int chunk = copy ? blockIdx.x - new_chunks : blockIdx.x;
   bool bad = s >= c.max_seqs || first < 0 || count < 0 || count > L || first > c.max_rows() - count;
-  if (copy && cow_src < 0 && cow_dst < 0) return;
-  bad = bad || (copy && (cow_src < 0 || cow_dst < 0 || cow_src >= c.n_pages || cow_dst >= c.n_pages));
-  if (bad) {
+  const bool none = cow_src < 0 && cow_dst < 0;
+  bad = bad || (!none && (cow_src < 0 || cow_dst < 0 || cow_src >= c.n_pages || cow_dst >= c.n_pages));
+  if (bad) {  // every chunk of the entry finds the same
     if (threadIdx.x == 0) flag(status, kDevErrBounds);
     return;
   }
+  if (copy && none) return;
   const int vec = threadIdx.x % kVecs;
   const int row0 = chunk * kRowsPerPass * kPasses + threadIdx.x / kVecs;
   const int rows = copy ? first % c.ps : count;
