@@ -78,3 +78,33 @@ def test_a_captured_step_takes_the_list_as_it_is_replayed(svg):
                 assert torch.equal(got[0], k[i, :, :n]) and torch.equal(got[1], v[i, :, :n])
     assert cache.lens.tolist() == [11, 11, 0, 0, 8, 0]
     assert svg.svg_get_device_status() == (svg.SVG_OK, 0)
+
+
+def test_a_full_pool_is_told_by_check(svg):
+    """Without room nothing is reserved or written, and attend reads the rows that were there."""
+    from video_dit_spatial_b200.layer import HistoryCache
+    cache = HistoryCache(1, 4, 16, 2, 2, 64, 3, 128, 2, 16)
+    k, v = rows(2, 2, 16, 64), rows(2, 2, 16, 64)
+    seqs, q, o = dev([0, 1]), rows(2, 2, 16, 64), rows(2, 2, 16, 64)
+    cache.reserve(seqs, dev([16, 16]))
+    cache.check()
+    cache.write(0, k, v)
+    cache.attend(0, q, seqs, 0, 0, o)
+    want = o.clone()
+    held = [[x.clone() for x in pool] for pool in cache.pools] + [[x.clone() for x in cache._state]]
+    cache.reserve(seqs, dev([16, 17]))  # three pages of two
+    cache.write(0, v, k)
+    cache.attend(0, q, seqs, 0, 0, o)
+    with pytest.raises(svg.SvgError) as e:
+        cache.check()
+    assert e.value.status == svg.SVG_ERR_CAPACITY
+    cache.check()  # told once
+    for now, before in zip(cache.pools + [cache._state], held):
+        assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(now, before))
+    assert torch.equal(o, want)
+    cache.reserve(seqs, dev([16, 16]))
+    cache.check()
+    cache.fork(dev([0]), dev([9]))
+    with pytest.raises(svg.SvgError) as e:
+        cache.check()
+    assert e.value.status == svg.SVG_ERR_INVALID_ARG

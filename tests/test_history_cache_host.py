@@ -45,3 +45,15 @@ def test_write_names_the_sequences_that_reserve_was_given(calls):
     cache.fork(ints([0]), ints([5]))
     with pytest.raises(ValueError, match="follows reserve"):
         cache.write(0, rows[:1], rows[:1])
+
+
+def test_check_raises_what_the_device_refused(calls, monkeypatch):
+    cache = HistoryCache(1, 8, 16, 2, 1, 64, 6, 64, 3, 8, device="cpu")
+    for status in (svg.SVG_ERR_CAPACITY, svg.SVG_ERR_INVALID_ARG, svg.SVG_ERR_DEVICE_TIMEOUT,
+                   svg.SVG_ERR_CUDA):
+        monkeypatch.setattr(svg, "svg_get_device_status", lambda stream: (status, 0))
+        with pytest.raises(svg.SvgError) as e:
+            cache.check()
+        assert e.value.status == status
+    monkeypatch.setattr(svg, "svg_get_device_status", lambda stream: (svg.SVG_OK, stream))
+    cache.check(stream=7)

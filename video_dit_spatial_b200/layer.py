@@ -345,6 +345,12 @@ class HistoryCache:
       fork(src, dst)            continuations of one history, sharing its pages
       free(seqs, keep)          a sequence dropped, or cut back to its first rows
       compact()                 the pages in use moved to the front of the pools
+      check()                   an error if any of these was refused on the device
+
+    What depends on the state is refused on the device, with no word from the call itself: a reserve
+    without enough free pages reserves nothing, after which write writes nothing and attend
+    reads the lengths as they were. check() tells, at the price of a wait: call it after
+    reserve where the pools may run out, or once a chunk.
 
     seqs, counts, src, dst and keep are device int32 tensors; negative sequence
     numbers are idle entries of a padded batch. One cache is used by one stream
@@ -394,6 +400,7 @@ class HistoryCache:
         self._planned = 0  # the plan's rows may be gone
 
     def reserve(self, seqs, counts, stream=None) -> None:
+        """All of it or, where the pools have too few free pages, nothing (see check)."""
         from . import svg_cache_reserve
         svg_cache_reserve(self.geom, *self._state, seqs, counts, self.plan, stream=stream)
         # write pairs the plan with these numbers, whatever the caller's list holds by then
@@ -401,6 +408,16 @@ class HistoryCache:
         with _on_stream(stream):
             self._numbers[:n].copy_(seqs.view(-1))
         self._planned = n
+
+    def check(self, stream=None) -> None:
+        """Waits for the stream and raises SvgError if something was refused on the current
+        device since the status was last read (by this or by svg_get_device_status):
+        SVG_ERR_CAPACITY where reserve had no room, SVG_ERR_INVALID_ARG for a sequence
+        number or a state that cannot be, SVG_ERR_DEVICE_TIMEOUT. Not while a graph is captured."""
+        from . import SVG_OK, SvgError, svg_get_device_status
+        status, _ = svg_get_device_status(stream)
+        if status != SVG_OK:
+            raise SvgError("HistoryCache", status)
 
     def write(self, layer: int, k_new, v_new, stream=None) -> None:
         """k_new, v_new [n, H_kv, L, d]: the rows that the last reserve made room for."""
