@@ -57,3 +57,18 @@ def test_check_raises_what_the_device_refused(calls, monkeypatch):
         assert e.value.status == status
     monkeypatch.setattr(svg, "svg_get_device_status", lambda stream: (svg.SVG_OK, stream))
     cache.check(stream=7)
+
+
+def test_attention_without_a_workspace_is_a_status():
+    """As every other null, and as an address whose size is not given."""
+    from video_dit_spatial_b200 import _build
+    _build.build()
+    geom = svg.CacheGeom(8, 16, 2, 64, 4, 5)
+    for workspace, size, status in ((None, None, svg.SVG_ERR_INVALID_ARG),
+                                    (None, 1 << 30, svg.SVG_ERR_INVALID_ARG),
+                                    (256, None, svg.SVG_ERR_CAPACITY),
+                                    (256, 64, svg.SVG_ERR_CAPACITY)):
+        with pytest.raises(svg.SvgError) as e:
+            svg.svg_prefix_attention(geom, 2, 4, 3, 0, 17, 0.1, 1 << 20, 256, 256, 256, 256, 256, 256,
+                                     None, workspace, workspace_bytes=size)
+        assert e.value.status == status

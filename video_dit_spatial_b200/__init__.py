@@ -513,9 +513,11 @@ def svg_prefix_attention(geom: CacheGeom, B, H, Lq, prefix_seq, prefix_len, scal
                          stream=None) -> None:
     torch, dev = _here()
     i32, bf16, rows, values = torch.int32, torch.bfloat16, B * H * Lq, _pool_values(geom)
-    wb = _nbytes(workspace) if workspace_bytes is None else workspace_bytes
-    ws = _buf("workspace", workspace, workspace.dtype, 0, dev) \
-        if workspace.__class__ is not int else workspace
+    ws, wb = workspace, workspace_bytes
+    if ws is None or ws.__class__ is int:  # an address comes with its size
+        wb = 0 if wb is None else wb
+    else:
+        ws, wb = _buf("workspace", ws, ws.dtype, 0, dev), _nbytes(ws) if wb is None else wb
     _check("svg_prefix_attention", load().svg_prefix_attention(
         ctypes.byref(geom), B, H, Lq, prefix_seq, prefix_len, scale,
         _buf("q", q, bf16, rows * geom.head_dim, dev),
