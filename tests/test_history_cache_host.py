@@ -72,3 +72,17 @@ def test_attention_without_a_workspace_is_a_status():
             svg.svg_prefix_attention(geom, 2, 4, 3, 0, 17, 0.1, 1 << 20, 256, 256, 256, 256, 256, 256,
                                      None, workspace, workspace_bytes=size)
         assert e.value.status == status
+
+
+def test_a_device_that_is_not_current_is_refused_before_anything_is_allocated(calls, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    def no(*a, **kw):
+        raise AssertionError("allocated")
+
+    monkeypatch.setattr(torch, "empty", no)
+    with pytest.raises(ValueError, match="make cuda:1 the current one"):
+        HistoryCache(1, 8, 16, 2, 1, 64, 6, 64, 3, 8, device="cuda:1")
+    for device in ("cuda", "cuda:0"):
+        with pytest.raises(AssertionError, match="allocated"):
+            HistoryCache(1, 8, 16, 2, 1, 64, 6, 64, 3, 8, device=device)

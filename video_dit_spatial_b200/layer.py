@@ -360,12 +360,17 @@ class HistoryCache:
     def __init__(self, n_layers: int, n_pages: int, page_size: int, H: int, H_kv: int, d: int,
                  max_seqs: int, max_rows: int, batch: int, rows: int, scale=None, device="cuda"):
         """max_rows: of one sequence, at most 2^20; batch, rows: the most sequences and query
-        rows a sequence that one call of reserve, write or attend has."""
+        rows a sequence that one call of reserve, write or attend has. device: the current one,
+        here and in every call, as everywhere in this library; the pools are set up on its
+        current stream."""
         from . import CacheGeom, svg_cache_reset, svg_prefix_attention_workspace_bytes
+        dev = self.device = torch.device(device)
+        if dev.type == "cuda" and dev.index is not None and dev.index != torch.cuda.current_device():
+            raise ValueError(f"the current device is cuda:{torch.cuda.current_device()}: make {dev} the "
+                             f"current one (torch.cuda.device) for a cache there")
         self.geom = CacheGeom(n_pages, page_size, H_kv, d, max_seqs, -(-max_rows // page_size))
         self.H = H
         self.scale = float(d ** -0.5 if scale is None else scale)
-        dev = self.device = torch.device(device)
         need = svg_prefix_attention_workspace_bytes(self.geom, batch, H, rows)
         self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         i32 = dict(dtype=torch.int32, device=dev)
