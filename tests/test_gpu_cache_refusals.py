@@ -81,3 +81,21 @@ def test_write_of_a_bad_plan_writes_nothing(svg, plan):
     for x, y in zip(pools, before):
         y[0, :, 5:7] = 1.0  # the other entry of the call
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("n,width", [(4, 1 << 16), (1024, 257), (1, 40)])
+def test_far_more_pages_wanted_than_there_are(svg, n, width):
+    """Every entry wants its whole table row: nothing is reserved; what is free can be had after."""
+    geom = svg.CacheGeom(37, 16, 1, 64, n, width)
+    st = [torch.full((n, width), -1, dtype=torch.int32, device="cuda"), dev([0] * n), dev([0] * 37)]
+    seqs, plan = torch.arange(n, dtype=torch.int32, device="cuda"), dev([[9] * 4] * n)
+    svg.svg_cache_reserve(geom, *st, seqs, torch.full_like(seqs, 16 * width), plan)
+    assert svg.svg_get_device_status()[1] == 4
+    assert torch.all(st[0] == -1) and not st[1].any() and not st[2].any()
+    assert torch.equal(plan.cpu(), torch.tensor([[0, 0, -1, -1]] * n, dtype=torch.int32))
+    counts = torch.zeros_like(seqs)
+    counts[n - 1] = 16 * 37
+    svg.svg_cache_reserve(geom, *st, seqs, counts, plan)
+    assert svg.svg_get_device_status()[1] == 0
+    assert st[0][n - 1, :37].tolist() == list(range(37)) and torch.all(st[2] == 1)
+    assert plan[n - 1].tolist() == [0, 16 * 37, -1, -1] and st[1].tolist() == counts.tolist()

@@ -122,23 +122,22 @@ constexpr int kPer = 16;                      // pages a thread looks at per ste
 constexpr int kStep = kOneThreads * kPer;     // pages the CTA looks at per step
 
 // Inclusive sum over the CTA's threads; `total` gets the whole sum.
-template <typename T>
-__device__ __forceinline__ T block_sum_scan(T v, T* warp_sums, T& total) {
+__device__ __forceinline__ int block_sum_scan(int v, int* warp_sums, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  T x = v;
+  int x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const T y = __shfl_up_sync(0xffffffffu, x, o);
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   __syncthreads();  // warp_sums free again
   if (lane == 31) warp_sums[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    T w = warp_sums[lane];
+    int w = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const T y = __shfl_up_sync(0xffffffffu, w, o);
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
       if (lane >= o) w += y;
     }
     warp_sums[lane] = w;
@@ -180,7 +179,6 @@ __global__ void __launch_bounds__(kOneThreads)
   __shared__ int s_seq[kOneThreads], s_off[kOneThreads], s_slot[kOneThreads];
   __shared__ uint16_t s_free[kStep];  // the step's free pages, ascending, relative to its first
   __shared__ int warp_sums[32];
-  __shared__ long long wide_sums[32];  // 1024 entries may want more than 2^31 pages between them
   const int tid = threadIdx.x;
   int s = -1, add = 0, len = 0, open = -1, slot = 0, need = 0;
   bool cow = false;
@@ -226,9 +224,10 @@ __global__ void __launch_bounds__(kOneThreads)
       cow = false;
     }
   }
-  long long total;
-  const long long off = block_sum_scan<long long>(need, wide_sums, total) - need;
-  s_off[tid] = off < c.n_pages ? static_cast<int>(off) : c.n_pages;
+  // An entry wants max_pages pages at most and no sequence has two entries that want any: the sum
+  // is at most max_seqs * max_pages, which fits 32 bits.
+  int total;
+  s_off[tid] = block_sum_scan(need, warp_sums, total) - need;
   s_slot[tid] = slot;
   // pass 0 counts the free pages, pass 1 hands them out
   bool enough = total == 0;
