@@ -598,8 +598,10 @@ svg_status svg_prefix_attention_workspace_bytes(const svg_cache_geom* geom, int3
  * row i and head h (key head h / (H / H_kv)), the keys are rows
  * [0, prefix_len) of sequence prefix_seq and rows [prefix_len, lens[s]) of
  * sequence s:
- *   O[b,h,i] = sum_j softmax_j(scale * q[b,h,i] . k_j) v_j,
- * accumulated in fp32, rounded to bf16. Where the entries have few query rows,
+ *   O[b,h,i] = sum_j softmax_j(scale * q[b,h,i] . k_j) v_j.
+ * Scores, maxima, sums and O are held in fp32; the weights are rounded to bf16 for
+ * their product with the values (off by at most 2^-8 of each, as in
+ * svg_sparse_attention), and O once at the end. Where the entries have few query rows,
  * the rows of all of them are gathered into tiles and the shared keys and
  * values are read once for all; a fork of one history gives such sequences.
  * The prefix need not end with a page. Rows past a sequence's
