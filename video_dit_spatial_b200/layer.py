@@ -322,7 +322,7 @@ class SemanticSparseLayer:
 
 
 def _on_stream(stream):
-    """Context in which torch works on `stream`: a stream, its handle, or None for the current one."""
+    """Context in which torch works on `stream`: a stream or its handle."""
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     return torch.cuda.stream(stream)
@@ -410,8 +410,12 @@ class HistoryCache:
         svg_cache_reserve(self.geom, *self._state, seqs, counts, self.plan, stream=stream)
         # write pairs the plan with these numbers, whatever the caller's list holds by then
         n = seqs.numel()
-        with _on_stream(stream):
-            self._numbers[:n].copy_(seqs.view(-1))
+        numbers = self._numbers if n == self._numbers.numel() else self._numbers[:n]
+        if stream is None:
+            numbers.copy_(seqs.view(n))
+        else:
+            with _on_stream(stream):
+                numbers.copy_(seqs.view(n))
         self._planned = n
 
     def check(self, stream=None) -> None:
@@ -435,8 +439,8 @@ class HistoryCache:
             raise ValueError(f"rows of shape {tuple(k_new.shape)} and {tuple(v_new.shape)} for "
                              f"{self._planned} sequences, {self.geom.H_kv} heads of "
                              f"{self.geom.head_dim}")
-        svg_cache_write(self.geom, self.table, self._numbers[:n], self.plan, k_new.shape[2], k_new,
-                        v_new, *self.pools[layer], stream=stream)
+        svg_cache_write(self.geom, self.table, self._numbers, self.plan, k_new.shape[2], k_new, v_new,
+                        *self.pools[layer], n=n, stream=stream)
 
     def compact(self, stream=None) -> None:
         from . import svg_cache_compact, svg_cache_copy_pages
