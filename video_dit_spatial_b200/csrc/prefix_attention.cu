@@ -953,14 +953,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Items of up to 16 rows: one row of a few sequences over a long prefix, or one
 // sequence's rows over its own keys. Their products are too small for a
 // 128-row tensor-memory tile to pay: its softmax keeps one warp busy (2.1k cycles a
-// block) and holds a V buffer meanwhile, so that it ran at 3.2k cycles for 64 KB (3.4 TB/s)
-// and took some 20k for a tail of three blocks. What bounds the work is
+// block) and holds a V buffer meanwhile. What bounds the work is
 // reading K and V once. So one CTA per SM streams them through a ring of
 // 128 KB, across the borders of items, and four warps take 16 keys (32 at d = 64) of each
 // block with mma.sync m16n8k16 (the four joined at the end of a piece):
 // a block's 32 KB take 1.4k cycles from HBM, its products and softmax 1.1k of each warp, the
 // end of an item 1.8k. One row of 16 sequences over 118800 shared rows, 24 heads,
-// d = 128: 241 us for 1.55 GB, 6.4 TB/s.
+// d = 128: 241 us for 1.55 GB, 6.4 TB/s; the whole call 248 us, and 374 us with the tile kernel
+// in this one's place.
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(

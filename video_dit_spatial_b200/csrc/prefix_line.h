@@ -19,8 +19,11 @@ constexpr int kMaxRounds = 16;       // in which items are dealt out
 constexpr int kFewRows = 16;    // rows of an item of the few-row kernel
 constexpr int kFewWarps = 4;    // that compute
 // Cost of a block: a two-tile block takes 3.4k to 3.7k cycles of products and
-// exponentials, a one-tile block takes about as long as its
-// 64 KB take from HBM on every SM at once, 2.8k.
+// exponentials at either head width. A one-tile block takes at d = 128 about as long as its
+// 64 KB take from HBM on every SM at once, 2.8k; at d = 64, with 32 KB, less: 32 rows over 60000
+// shared rows, 24 heads, 76 blocks a CTA, take 132 us at d = 128 and 91 us at d = 64 (3.3k
+// and 2.3k cycles a block, beginning and end of the call included). The units are those of
+// d = 128 for both: at d = 64 a one-tile block costs up to a third less than they say.
 constexpr int kCostTwo = 4, kCostOne = 3;
 
 // Keys of a block of the few-row kernel.
@@ -198,6 +201,10 @@ __host__ __device__ inline int64_t rest_begin(const Sizes& z, const int64_t* cum
 // query heads to a key head, 79 and 59 us; of 40 over 20000 and 64, 24 heads, 82 and 70 us.
 // (Without the tile kernel's items: rows of 150 over 700 and up to 30, eight heads to a key
 // head, 54 us instead of 47.)
+// With the few-row kernel's work taken for 1/2, 2/3, 1, 4/3 and 2 times as much, in us: at d = 128 the
+// first of these calls 70 61 59 69 79, the second 101 84 71 71 76; at d = 64 the first 65 56 50 53
+// 59, the second 119 89 68 55 54, rows of 100 over 3000 and up to 200, two heads to a key head,
+// 48 44 41 47 59. No one share is the best at d = 64; the second call would want more of the SMs.
 __host__ __device__ inline int few_share(int n, int64_t blocks, int64_t items, int64_t tile_cost,
                                          int tile_items) {
   if (blocks == 0) return 0;
@@ -252,10 +259,18 @@ inline int group_cost(int rows, int group) {
   return (g - 1) * kCostTwo + cost_of(rows_of(rows, g - 1, group));
 }
 
-// Which kernel has which items. Rows of one sequence up to 16: its own keys go to
-// the few-row kernel, and the prefix too if all sequences' rows are up
+// Which kernel has which items. Rows of one sequence up to 16 (what a tile of mma.sync
+// holds): its own keys go to the few-row kernel, and the prefix too if all sequences' rows are up
 // to 16. Otherwise joint items, unless gathering all sequences' rows over the
 // prefix saves a tenth of it or more.
+// The same calls with the few-row kernel / with the tile kernel in its place, in us, at d = 64; at
+// d = 128 (query rows to a key head: 1, then 16):
+//   a prefix alone, 60000 rows, 24 heads          64 / 89, 64 / 88;    115 / 122, 117 / 132
+//   a prefix of 20001 and up to 700 own rows,     39 / 79, 106 / 192;  49 / 80, 112 / 182
+//     64 sequences, 8 key heads
+//   2000 to 3000 own rows after one shared row,   108 / 184, 117 / 176;  194 / 230, 284 / 252
+//     60 sequences, 16 key heads
+// so that 16 rows are right but for long rows of their own at d = 128.
 enum Form { kFew, kMixed, kGathered, kJoint };
 inline Form form_of(int B, int GL, bool prefix) {
   if (GL <= kFewRows) return B * GL <= kFewRows || !prefix ? kFew : kMixed;
