@@ -618,8 +618,9 @@ svg_status svg_prefix_attention_workspace_bytes(const svg_cache_geom* geom, int3
  * prefix_seq shorter than prefix_len sets the bounds bit; the entry's rows are
  * left as they are (with a bad prefix, every row is). A page number past the
  * pool sets it too, and its rows count as zeros.
- * A row without keys gets O = 0, lse = -inf, and so does one whose scores are all -inf; a
- * NaN or +inf among a row's scores makes its O and lse NaN and reaches no other row.
+ * A row without keys gets O = 0, lse = -inf, and so does one whose scores are all -inf
+ * (over finite values); a NaN or +inf among a row's scores makes its O and lse NaN and
+ * reaches no other row.
  * Same results on every call: no atomics in the arithmetic.
  * Errors: as above, and INVALID_ARG (B < 1 or > 1024, Lq < 1, H not a multiple
  * of H_kv, B * H * Lq > 2^31 - 1, max_pages * page_size > 2^20 (further than

@@ -108,3 +108,20 @@ def test_a_full_pool_is_told_by_check(svg):
     with pytest.raises(svg.SvgError) as e:
         cache.check()
     assert e.value.status == svg.SVG_ERR_INVALID_ARG
+
+
+def test_a_stream_of_another_kind(svg):
+    """Whatever has a cuda_stream, as in every other call."""
+    from video_dit_spatial_b200.layer import HistoryCache
+
+    class Other:
+        cuda_stream = torch.cuda.Stream().cuda_stream
+
+    cache = HistoryCache(1, 16, 16, 2, 2, 64, 6, 64, 3, 8)
+    seqs, counts, k, v = dev([4, 1]), dev([8, 5]), rows(2, 2, 8, 64), rows(2, 2, 8, 64)
+    torch.cuda.synchronize()
+    cache.reserve(seqs, counts, stream=Other)
+    cache.write(0, k, v, stream=Other)
+    cache.check(stream=Other)
+    for i, (s, n) in enumerate(((4, 8), (1, 5))):
+        assert all(torch.equal(x, y[i, :, :n]) for x, y in zip(rows_of(cache, 0, s, 0, n), (k, v)))

@@ -32,7 +32,7 @@ from typing import Optional
 
 import torch
 
-from . import (Geom, SVG_MASK_DENSE, SVG_MASK_SPATIAL, SVG_MASK_TEMPORAL, svg_build_block_mask,
+from . import (Geom, SVG_MASK_DENSE, SVG_MASK_SPATIAL, SVG_MASK_TEMPORAL, _stream, svg_build_block_mask,
                svg_mask_nnz, svg_permute_qkv, svg_profile_heads, svg_profile_workspace_bytes,
                svg_quantize_v_e4m3, svg_sparse_attention, svg_sparse_attention_fp8pv,
                svg_sparse_attention_fused, svg_unpermute)
@@ -322,9 +322,9 @@ class SemanticSparseLayer:
 
 
 def _on_stream(stream):
-    """Context in which torch works on `stream`: a stream or its handle."""
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+    """Context in which torch works on `stream`, of any kind that the calls take."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream))
     return torch.cuda.stream(stream)
 
 
