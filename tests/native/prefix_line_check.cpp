@@ -116,6 +116,7 @@ int check_line(const Sizes& z, int bk, int few_bk, const int* lens, bool ok_pref
 extern "C" int check_call(int B, int H_kv, int GL, int d, int prefix_len, int sms, const int* lens,
                           int ok_prefix, int* out) {
   const Form form = form_of(B, GL, prefix_len > 0);
+  sms = ctas_of(sms);
   for (int i = 0; i < 5; ++i) out[i] = 0;
   out[0] = form;
   if (form == kFew || form == kMixed) {

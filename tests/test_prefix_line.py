@@ -103,3 +103,11 @@ def test_the_largest_sums(check, d):
     check(1024, 2, 1, d, longest, [longest] * 1024)
     check(1024, 1, 300, d, longest // 2, [longest] * 1024)
     check(1, 1, 1 << 20, d, 1000, [1000 + longest // 2])
+
+
+@pytest.mark.parametrize("sms", [1, 2, 3, 148, 200])
+def test_any_number_of_sms(check, sms):
+    """A share of a device may have a single one; two kernels of a batch still get a CTA each."""
+    for B, H_kv, GL, prefix in ((9, 4, 4, 100), (2, 4, 4, 900), (7, 3, 31, 411), (3, 2, 300, 1000)):
+        for own in (0, 40, 700):
+            check(B, H_kv, GL, 128, prefix, [prefix + own * (b % 3) for b in range(B)], sms=sms)

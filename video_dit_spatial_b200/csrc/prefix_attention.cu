@@ -1533,7 +1533,7 @@ cudaError_t launch_prefix_attention(const PrefixArgs& a, int* status, cudaStream
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  if (sms > kMaxCtas) sms = kMaxCtas;
+  sms = ctas_of(sms);
   p.c = a.c;
   p.prefix_seq = a.prefix_seq;
   p.scale_log2 = a.scale * 1.4426950408889634f;

@@ -29,6 +29,13 @@ constexpr int kCostTwo = 4, kCostOne = 3;
 // Keys of a block of the few-row kernel.
 __host__ __device__ constexpr int few_block(int d) { return kFewWarps * 2048 / d; }
 
+// CTAs of a kernel on a device (or a share of one) with `sms` SMs: one each, but two at least, since
+// the two kernels of a mixed batch share them out and none may be left with no CTA. CTAs do not wait
+// for one another, so they need not be resident together.
+__host__ __device__ inline int ctas_of(int sms) {
+  return sms < 2 ? 2 : sms > kMaxCtas ? kMaxCtas : sms;
+}
+
 struct Sizes {
   int32_t n_ctas;   // CTAs launched
   int32_t B, H_kv, GL;
